@@ -18,3 +18,9 @@ from ._binding import (  # noqa: F401
     plan_build,
     workspace_size,
 )
+from ._serving import (  # noqa: F401
+    PagedCache,
+    rope,
+    rope_bwd,
+    tree_words,
+)

@@ -707,6 +707,8 @@ const char *bsa_status_string(bsa_status status) {
     case BSA_ERR_NO_DEVICE: return "no sm_100 device is current";
     case BSA_ERR_INPUT_RANGE:
       return "a backward input or dS entry lies beyond the fp16 range or is not finite";
+    case BSA_ERR_BAD_CACHE:
+      return "a paged cache's length, count of new tokens or page index is out of range";
   }
   return "unknown status";
 }

@@ -5,6 +5,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <algorithm>
 #include <utility>
 #include <cuda.h>
 #include <cuda_runtime.h>

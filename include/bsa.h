@@ -75,10 +75,13 @@ typedef enum bsa_status {
   BSA_ERR_BAD_MASK_DATA = 7,       /* device: cu_seqlens not [0 .. Sq] non-decreasing */
   BSA_WARN_GATE_VIOLATION = 8,     /* device: a gated fixed-m row summed below 2^-100 */
   BSA_ERR_NO_DEVICE = 9,           /* no sm_100 device current                        */
-  BSA_ERR_INPUT_RANGE = 10         /* device: a backward input (Q, K, V, dO) or an
+  BSA_ERR_INPUT_RANGE = 10,        /* device: a backward input (Q, K, V, dO) or an
                                       entry of dS lies beyond the fp16 range
                                       (|x| >= 65504) or is not finite; the
                                       backward takes its products in fp16 */
+  BSA_ERR_BAD_CACHE = 11           /* device: a paged cache's length, count of new
+                                      tokens or page index is out of range (clamped
+                                      or skipped, see bsa_cache)                 */
 } bsa_status;
 
 /* Block-map tile edge (rows and keys). */
@@ -435,6 +438,169 @@ BSA_API bsa_status bsa_get_device_status(void *ws, size_t ws_bytes, bsa_stream_t
  * softmax.  Synchronises `stream`, like bsa_get_device_status.  Errors:
  * INVALID_ARG (null or too small a workspace), CUDA. */
 BSA_API bsa_status bsa_fixed_rows(void *ws, size_t ws_bytes, bsa_stream_t stream, uint64_t *rows);
+
+/* ---------------------------------------------------------------------------
+ * Positions and the paged cache: what a serving loop does around the attention
+ * (rotate and append, attend, weigh, evict), and the rotary positions of
+ * training with their backward.
+ * ------------------------------------------------------------------------- */
+
+#define BSA_DTYPE_BF16 0
+#define BSA_DTYPE_FP16 1
+
+/* Rotary pairs: pair p is the elements (2p, 2p+1), or (p, p + n_pairs). */
+#define BSA_ROPE_INTERLEAVED 0
+#define BSA_ROPE_HALVES 1
+
+/* Rotary positions with up to 8 axes (time, height, width, ...):
+ *   angle(b, t, p) = pos[axis[p], b, t] * inv_freq[p]        (radians)
+ *   y0 = x0 cos - x1 sin,  y1 = x0 sin + x1 cos
+ * for the pairs p < n_pairs; elements at or past 2 n_pairs are copied, and so
+ * is a pair whose axis entry lies outside [0, n_axes).  inverse = 1 rotates
+ * back by the same angles, which is the gradient: dx = R(-angle) dy.  The angle
+ * is reduced to a turn in 64-bit fixed point, so it is as exact at position
+ * 2^31 - 1 as at position 1.  A frequency that is not finite counts as 0. */
+typedef struct bsa_rope_spec {
+  int32_t n_axes;          /* 1 .. 8                                              */
+  int32_t n_pairs;         /* 1 .. D/2; HALVES: a multiple of 8                   */
+  int32_t layout;          /* BSA_ROPE_*                                          */
+  int32_t inverse;         /* 0 or 1                                              */
+  const double *inv_freq;  /* device [n_pairs], radians per position              */
+  const int32_t *axis;     /* device [n_pairs]                                    */
+  const int32_t *pos;      /* device, pos[a*pos_stride[0] + b*pos_stride[1] + t]  */
+  int64_t pos_stride[2];   /* elements; both 0 = contiguous [n_axes, B, T]        */
+} bsa_rope_spec;
+
+/* T tokens of each of B sequences: q [B, T, H, D], k and v [B, T, H_kv, D], the
+ * head dimension contiguous. */
+typedef struct bsa_tokens {
+  int32_t B;               /* >= 0                                                */
+  int32_t T;               /* >= 0; bsa_cache_attend and bsa_cache_weigh: <= 64    */
+  int32_t H;               /* query heads, >= 1                                   */
+  int32_t H_kv;            /* key/value heads, 0 = H; H a multiple of it          */
+  int32_t D;               /* bsa_rope: a multiple of 16 up to 256; else 64, 128   */
+  int32_t dtype;           /* BSA_DTYPE_*                                         */
+  /* element strides (batch, token, head), multiples of 8; all zero = contiguous.
+   * qo_stride: q_out / out; ko_stride: k_out of bsa_rope. */
+  int64_t q_stride[3];
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  int64_t qo_stride[3];
+  int64_t ko_stride[3];
+  float scale;             /* of the products; <= 0: 1/sqrt(D)                    */
+  int32_t reserved;
+  const int32_t *n_new;    /* device [B]: the tokens of each sequence that are
+                              real, the first n_new[b] of its T; NULL = all T.
+                              Outside [0, T] it is clamped (BSA_ERR_BAD_CACHE)     */
+  const int64_t *tree;     /* device [B, T] or NULL: bit j of word t says that
+                              token t sees token j of its sequence's new tokens;
+                              NULL: a chain, token t sees tokens 0 .. t           */
+} bsa_tokens;
+
+/* A paged key/value cache: slot s of sequence b is row s mod page_size of page
+ * page_table[b, s / page_size].  `length` counts the slots in use before the T
+ * new tokens of a call, whose own slots are length[b] .. length[b]+n_new[b]-1;
+ * no call but bsa_cache_evict changes it.  Device-side checks, reported in the
+ * workspace's status word as BSA_ERR_BAD_CACHE: a length outside [0, capacity]
+ * or with its new tokens past the capacity max_pages * page_size is clamped; a
+ * page index outside [0, n_pages) reads as zeros and is never written.  Slots
+ * that are not in use may hold anything, NaN included.  Sequences may share
+ * pages that are only read; append and evict write in place, so the pages they
+ * write belong to one sequence. */
+typedef struct bsa_cache {
+  int32_t n_pages;         /* 1 .. 2^30                                           */
+  int32_t page_size;       /* slots per page: a power of two, 8 .. 65536           */
+  int32_t H_kv;
+  int32_t D;               /* 64 or 128                                           */
+  int32_t dtype;           /* BSA_DTYPE_*                                         */
+  int32_t B;               /* sequences                                           */
+  int32_t max_pages;       /* page_table's entries per sequence; capacity <= 2^30  */
+  int32_t reserved;
+  void *k, *v;             /* device [n_pages, page_size, H_kv, D], 16-byte aligned */
+  int64_t k_stride[3];     /* elements (page, slot, head), multiples of 8; zero =
+                              contiguous                                          */
+  int64_t v_stride[3];
+  const int32_t *page_table;  /* device [B, max_pages]                            */
+  int64_t table_stride;    /* elements between sequences; 0 = max_pages           */
+  const int32_t *length;   /* device [B]                                          */
+} bsa_cache;
+
+typedef struct bsa_evict_spec {
+  int32_t budget;          /* slots each head keeps, >= 1                         */
+  int32_t sinks;           /* keep pos < sinks                                    */
+  int32_t recent;          /* keep pos >= next_pos[b] - recent                    */
+  int32_t reserved;
+  const int32_t *next_pos; /* device [B]: the position of the sequence's next token */
+  /* device [B, H_kv, capacity]; the outputs may be the inputs */
+  const float *score_in;
+  const int32_t *pos_in;
+  float *score_out;
+  int32_t *pos_out;
+  int32_t *length_out;     /* device [B]; may be the cache's length               */
+} bsa_evict_spec;
+
+/* Rotates q [B, T, H, D] into q_out and k [B, T, H_kv, D] into k_out, either
+ * pair NULL to leave it out (q_out = q and k_out = k rotate in place; otherwise
+ * input and output do not overlap).  One launch, no workspace.
+ * Errors: INVALID_ARG (null pointers, sizes, n_axes, n_pairs, layout or inverse
+ * out of range), UNSUPPORTED (D, dtype, a stride not a multiple of 8 elements, a
+ * tensor not 16-byte aligned), NO_DEVICE, CUDA.  B == 0 or T == 0: a checked no-op. */
+BSA_API bsa_status bsa_rope(const bsa_tokens *tok, const bsa_rope_spec *rope, const void *q, void *q_out,
+                            const void *k, void *k_out, bsa_stream_t stream);
+
+/* Bytes of the workspace the cache calls need (bsa_cache_evict: for any budget
+ * up to the given one; the other calls take budget = 0).  Zero its first 256
+ * bytes before its first use (bsa_get_device_status with clear = 1 does for a
+ * sticky status).  Calls that share a workspace run one after the other on one
+ * stream.  256-byte aligned; host arithmetic only, but for the device's number
+ * of SMs (the largest such number where no device is current). */
+BSA_API bsa_status bsa_cache_workspace_size(const bsa_cache *cache, int32_t budget, size_t *bytes);
+
+/* The new tokens into the cache: k (rotated when `rope` is given) and v into the
+ * slots length[b] + t, t < n_new[b]; q (NULL to leave it out), every row of it,
+ * rotated into q_out (q_out = q: in place).  One launch.  Errors as for
+ * bsa_rope, with INVALID_ARG also for tokens that do not match the cache and
+ * WORKSPACE_TOO_SMALL. */
+BSA_API bsa_status bsa_cache_append(const bsa_cache *cache, const bsa_tokens *tok, const bsa_rope_spec *rope,
+                                    const void *q, void *q_out, const void *k, const void *v, void *ws,
+                                    size_t ws_bytes, bsa_stream_t stream);
+
+/* Attention of T <= 64 new tokens (a tree of drafted tokens, or one) over the
+ * cache, which holds them already: token t of sequence b sees the slots below
+ * length[b] and the new tokens its tree word names (bits at or past n_new[b]
+ * are ignored).  out [B, T, H, D] (qo_stride), lse fp32 [B, H, T] contiguous.
+ * A row that sees nothing, and every row t >= n_new[b], is written as 0 / -inf.
+ * K and V of what a row does not see never reach it, NaN and infinities
+ * included.  The same inputs give the same bits.
+ * Errors as for bsa_cache_append; INVALID_ARG also for T > 64, UNSUPPORTED for
+ * H / H_kv > 128. */
+BSA_API bsa_status bsa_cache_attend(const bsa_cache *cache, const bsa_tokens *tok, const void *q, void *out,
+                                    float *lse, void *ws, size_t ws_bytes, bsa_stream_t stream);
+
+/* Accumulated attention weight: for every slot j < length[b] + n_new[b] and key
+ * head, score_out = score_in + the sum over the tokens t < n_new[b] and the
+ * query heads h of the group that see j of exp(scale q.k_j - lse[b, h, t]).
+ * score [B, H_kv, capacity] fp32 (score_out may be score_in; other slots are
+ * left as they are); lse as bsa_cache_attend wrote it (-inf: the row adds
+ * nothing).  The same inputs give the same bits.  Errors as for
+ * bsa_cache_attend. */
+BSA_API bsa_status bsa_cache_weigh(const bsa_cache *cache, const bsa_tokens *tok, const void *q,
+                                   const float *lse, const float *score_in, float *score_out, void *ws,
+                                   size_t ws_bytes, bsa_stream_t stream);
+
+/* Each (sequence, key head) with more than `budget` slots keeps `budget` of
+ * them: first those with pos < sinks or pos >= next_pos[b] - recent, then by
+ * score, highest first; equal ones go to the lower slot (a NaN counts as the
+ * lowest score, -0 as 0).  The kept slots at or past the budget move into the
+ * dropped ones below it, the i-th into the i-th in slot order, with their K, V,
+ * score and pos; the others stay where they are, so a key's position is what
+ * `pos` says and not its slot.  Then score_out and pos_out hold the kept slots
+ * in [0, budget), 0 and -1 in [budget, length), and length_out[b] =
+ * min(length[b], budget).  A sequence within the budget keeps all (copied when
+ * the outputs are not the inputs).  Slots past the length are left as they are.
+ * Errors as for bsa_cache_append. */
+BSA_API bsa_status bsa_cache_evict(const bsa_cache *cache, const bsa_evict_spec *spec, void *ws,
+                                   size_t ws_bytes, bsa_stream_t stream);
 
 /* Static description of a status code. */
 BSA_API const char *bsa_status_string(bsa_status status);
