@@ -104,10 +104,10 @@ EncodeTiledFn get_encode() {
 }
 
 // 4-D map over a 16-bit [B, S, H, D] tensor (bf16, or fp16 for the backward's
-// converted copies): dims (D, S, H, B), 64 x 128 boxes, 128-byte swizzle.
+// converted copies): dims (D, S, H, B), 64 x box_rows boxes, 128-byte swizzle.
 // Out-of-range rows read as zero.
 bool make_map(CUtensorMap *map, const void *ptr, int B, int S, int H, int D,
-              const int64_t *stride, bool fp16 = false) {
+              const int64_t *stride, bool fp16 = false, int box_rows = kTile) {
   auto enc = get_encode();
   if (enc == nullptr) return false;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(S),
@@ -115,7 +115,7 @@ bool make_map(CUtensorMap *map, const void *ptr, int B, int S, int H, int D,
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(stride[1]) * 2,
                                  static_cast<cuuint64_t>(stride[2]) * 2,
                                  static_cast<cuuint64_t>(stride[0]) * 2};
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(kTile), 1, 1};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = enc(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                          const_cast<void *>(ptr), dims,
@@ -420,6 +420,11 @@ cudaError_t plan_and_bound(const bsa_problem &p, const bsa_mask_spec &m, const b
 }
 
 }  // namespace
+
+bool make_cache_map(CUtensorMap *map, const void *ptr, int n_pages, int page_size, int H_kv, int D,
+                    const int64_t *stride, bool fp16) {
+  return make_map(map, ptr, n_pages, page_size, H_kv, D, stride, fp16, std::min(page_size, kTile));
+}
 
 // The forward call.  side_stream_ok = false keeps the plan and the bound on
 // `stream` one after the other (the static-scratch entry makes no call that

@@ -91,6 +91,13 @@ struct WsLayout {
 
 WsLayout compute_layout(const bsa_problem &p);
 
+// 4-D tensor map over a paged cache's K or V [n_pages, page_size, H_kv, D]
+// (strides page, slot, head in elements): dims (D, slot, head, page), boxes of 64
+// elements x min(page_size, 128) slots, 128-byte swizzle; a page past the end
+// reads as zero.
+bool make_cache_map(CUtensorMap *map, const void *ptr, int n_pages, int page_size, int H_kv, int D,
+                    const int64_t *stride, bool fp16);
+
 // Plan signature words (B, Sq, Skv, flags, window, order, n_seqs, dilation)
 // the planner stores in the header and every kernel that reads the plan checks.
 constexpr int kSigWords = 8;

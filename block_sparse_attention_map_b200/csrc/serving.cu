@@ -24,6 +24,12 @@ bool have_sm100() {
          cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) == cudaSuccess && major == 10;
 }
 
+bool sm_count(int *sms) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess &&
+         cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && *sms > 0;
+}
+
 // Contiguous strides where all three are zero, then the checks every tensor gets.
 bsa_status fix_strides(const int64_t *in, int64_t mid, int64_t heads, int64_t D, int64_t (&out)[3]) {
   if (in[0] == 0 && in[1] == 0 && in[2] == 0) {
@@ -94,13 +100,17 @@ bsa_status check_rope(const bsa_rope_spec *r, const bsa_tokens &t, bool empty, R
 
 // Where the workspace's parts lie.
 struct CacheWs {
-  size_t count, to, from, mpos, mscore, total;
+  size_t scratch;                        // attend's pieces
+  size_t count, to, from, mpos, mscore;  // evict's lists (they share the space: the calls follow one another)
+  size_t total;
   int list_cap;
 };
 
 CacheWs cache_ws(const CacheView &c, int budget) {
   CacheWs w{};
   const size_t heads = static_cast<size_t>(c.B) * c.H_kv;
+  w.scratch = kHeaderBytes;
+  const size_t attend_end = kHeaderBytes + up256(attend_scratch_bytes(c.D));
   size_t off = kHeaderBytes;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -117,7 +127,7 @@ CacheWs cache_ws(const CacheView &c, int budget) {
     w.mpos = take(list);
     w.mscore = take(list);
   }
-  w.total = off;
+  w.total = std::max(off, attend_end);
   return w;
 }
 
@@ -178,6 +188,10 @@ bsa_status check_reading(const bsa_cache *cache, const bsa_tokens *tok, CacheVie
   if ((st = check_tokens(tok, false, t)) != BSA_OK) return st;
   if (!matches(*cache, t->t) || t->t.T > kMaxTree) return BSA_ERR_INVALID_ARG;
   if (t->t.H / t->t.H_kv > kMaxGroup) return BSA_ERR_UNSUPPORTED;
+  // key tiles of all heads and row groups: 31 bits
+  const int64_t rows = static_cast<int64_t>(t->t.T) * (t->t.H / t->t.H_kv);
+  if (static_cast<int64_t>(c->B) * c->H_kv * (c->capacity / kTile + 1) >= (int64_t{1} << 31) / (rows / kTile + 1))
+    return BSA_ERR_UNSUPPORTED;
   if (!aligned4(t->t.n_new) || (reinterpret_cast<uintptr_t>(t->t.tree) & 7u)) return BSA_ERR_UNSUPPORTED;
   return BSA_OK;
 }
@@ -286,7 +300,15 @@ bsa_status bsa_cache_attend(const bsa_cache *cache, const bsa_tokens *tok, const
   copy3(a.os, t.qos);
   a.lse = lse;
   a.scale = t.t.scale;
-  return of_cuda(launch_attend(a, t.t.dtype == BSA_DTYPE_FP16, reinterpret_cast<cudaStream_t>(stream)));
+  a.scratch = static_cast<uint8_t *>(ws) + cache_ws(c, 0).scratch;
+  const bool fp16 = t.t.dtype == BSA_DTYPE_FP16;
+  CUtensorMap tk, tv;
+  if (!make_cache_map(&tk, c.k, c.n_pages, 1 << c.page_log, c.H_kv, c.D, c.ks, fp16) ||
+      !make_cache_map(&tv, c.v, c.n_pages, 1 << c.page_log, c.H_kv, c.D, c.vs, fp16))
+    return BSA_ERR_UNSUPPORTED;
+  int sms = 0;
+  if (!sm_count(&sms)) return BSA_ERR_NO_DEVICE;
+  return of_cuda(launch_attend(a, tk, tv, fp16, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 bsa_status bsa_cache_weigh(const bsa_cache *cache, const bsa_tokens *tok, const void *q, const float *lse,

@@ -96,8 +96,12 @@ struct AttendArgs {
   int64_t qs[3], os[3];
   float *lse;
   float scale;
+  uint8_t *scratch;  // attend_scratch_bytes(D)
 };
-cudaError_t launch_attend(const AttendArgs &a, bool fp16, cudaStream_t s);
+constexpr int kMaxCtas = 160;  // runs the attention is cut into, at most (one an SM)
+size_t attend_scratch_bytes(int D);
+cudaError_t launch_attend(const AttendArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, bool fp16, int sms,
+                          cudaStream_t s);
 
 struct WeighArgs {
   CacheView cache;

@@ -552,8 +552,8 @@ BSA_API bsa_status bsa_rope(const bsa_tokens *tok, const bsa_rope_spec *rope, co
  * up to the given one; the other calls take budget = 0).  Zero its first 256
  * bytes before its first use (bsa_get_device_status with clear = 1 does for a
  * sticky status).  Calls that share a workspace run one after the other on one
- * stream.  256-byte aligned; host arithmetic only, but for the device's number
- * of SMs (the largest such number where no device is current). */
+ * stream; caches whose calls all do may share one.  256-byte aligned; host
+ * arithmetic only. */
 BSA_API bsa_status bsa_cache_workspace_size(const bsa_cache *cache, int32_t budget, size_t *bytes);
 
 /* The new tokens into the cache: k (rotated when `rope` is given) and v into the
@@ -573,7 +573,8 @@ BSA_API bsa_status bsa_cache_append(const bsa_cache *cache, const bsa_tokens *to
  * K and V of what a row does not see never reach it, NaN and infinities
  * included.  The same inputs give the same bits.
  * Errors as for bsa_cache_append; INVALID_ARG also for T > 64, UNSUPPORTED for
- * H / H_kv > 128. */
+ * H / H_kv > 128 and for 2^31 or more tiles of 128 slots over all sequences, key
+ * heads and groups of 128 rows. */
 BSA_API bsa_status bsa_cache_attend(const bsa_cache *cache, const bsa_tokens *tok, const void *q, void *out,
                                     float *lse, void *ws, size_t ws_bytes, bsa_stream_t stream);
 
