@@ -26,7 +26,7 @@
 // (0 * NaN is NaN in the product), and a new token's infinities and NaN are taken
 // out of the tile and added back in the epilogue of the rows that see the token.
 // TMEM columns: S_0 [0,128) S_1 [128,256) O_0 [256,256+D) O_1 [256+D,256+2D).
-#include "serving.cuh"
+#include "runs.cuh"
 
 namespace bsa {
 namespace {
@@ -34,7 +34,6 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: tolerate p up to 2^8
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 struct AttendParams {
   CacheView cache;
@@ -47,105 +46,6 @@ struct AttendParams {
   int box_rows, box_log;  // keys of one TMA box: min(page_size, 128)
   float *part_o;          // [2 * CTAs, 128 * NX, D] unnormalised O of the pieces
   float4 *part_ml;        // [2 * CTAs, 128 * NX] maximum (log2), sum, sum of rounded weights
-};
-
-// ------------------------------------------------------------ the work list
-// Sequence b has H_kv * row_groups(b) items of tiles(b) key tiles each; the list
-// is all of them in order (b, kv head, row group, tile).
-template <int NX>
-struct Seq {
-  int len, n, tiles, groups;
-  __device__ __forceinline__ int64_t work(int H_kv) const { return static_cast<int64_t>(H_kv) * groups * tiles; }
-};
-
-template <int NX>
-__device__ __forceinline__ Seq<NX> sequence(const CacheView &c, const TokenView &t, int b, bool report) {
-  Seq<NX> s;
-  s.len = clamped_length(c, b, report);
-  s.n = clamped_new(c, t, b, s.len, report);
-  s.tiles = (s.len + s.n + kTile - 1) / kTile;
-  s.groups = (s.n * t.G + kTile * NX - 1) / (kTile * NX);
-  return s;
-}
-
-__device__ __forceinline__ int64_t run_start(int64_t total, int cta, int ctas) { return total * cta / ctas; }
-
-struct RunStart {
-  int b, item, tile, count;  // count: key tiles of the run
-};
-
-// Sum of work over the sequences, and the sequence that holds position `at`, by
-// one warp.
-template <int NX>
-__device__ __forceinline__ int64_t total_work(const AttendParams &p, int lane, bool report) {
-  int64_t sum = 0;
-  for (int b0 = 0; b0 < p.cache.B; b0 += 32)
-    if (b0 + lane < p.cache.B) sum += sequence<NX>(p.cache, p.tok, b0 + lane, report).work(p.cache.H_kv);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  return sum;
-}
-
-template <int NX>
-__device__ __forceinline__ RunStart find_start(const AttendParams &p, int64_t at, int count, int lane) {
-  RunStart r{0, 0, 0, count};
-  int64_t base = 0;
-  for (int b0 = 0; b0 < p.cache.B; b0 += 32) {
-    Seq<NX> s{0, 0, 0, 0};
-    if (b0 + lane < p.cache.B) s = sequence<NX>(p.cache, p.tok, b0 + lane, false);
-    const int64_t w = s.work(p.cache.H_kv);
-    int64_t incl = w;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += o;
-    }
-    const bool here = w > 0 && at >= base + incl - w && at < base + incl;
-    const uint32_t who = __ballot_sync(0xffffffffu, here);
-    if (who != 0u) {
-      const int src = __ffs(who) - 1;
-      const int64_t off = at - (base + incl - w);
-      const int item = here ? static_cast<int>(off / s.tiles) : 0, tile = here ? static_cast<int>(off % s.tiles) : 0;
-      r.b = b0 + src;
-      r.item = __shfl_sync(0xffffffffu, item, src);
-      r.tile = __shfl_sync(0xffffffffu, tile, src);
-      return r;
-    }
-    base += __shfl_sync(0xffffffffu, incl, 31);
-  }
-  r.count = 0;
-  return r;
-}
-
-// One CTA's run, piece by piece (a piece: consecutive key tiles of one item).
-template <int NX>
-struct Walk {
-  int b, item, tile, left, index;
-  Seq<NX> s;
-  int hk, rg, t0, t1;  // the piece: kv head, row group, key tiles [t0, t1)
-  bool whole;
-  __device__ __forceinline__ Walk(const AttendParams &p, const RunStart &r)
-      : b(r.b), item(r.item), tile(r.tile), left(r.count), index(-1) {
-    if (left > 0) s = sequence<NX>(p.cache, p.tok, b, false);
-  }
-  __device__ __forceinline__ bool next(const AttendParams &p) {
-    if (left <= 0) return false;
-    while (item >= p.cache.H_kv * s.groups) {
-      item = 0;
-      if (++b >= p.cache.B) return false;  // never, with lengths that stay as they are
-      s = sequence<NX>(p.cache, p.tok, b, false);
-    }
-    hk = item / s.groups;
-    rg = item % s.groups;
-    t0 = tile;
-    t1 = min(s.tiles, tile + left);
-    whole = t0 == 0 && t1 == s.tiles;
-    left -= t1 - t0;
-    tile = 0;
-    ++item;
-    ++index;
-    return true;
-  }
 };
 
 template <int D, int NX>
@@ -161,14 +61,6 @@ struct AttendSmem {
   static constexpr int kMisc = kRun + 16;              // tmem slot, abort flag
   static constexpr int kAlloc = kMisc + 16;
 };
-
-__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
-  const uint32_t a = smem_u32(bar);
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(a, parity)) {
-    if (globaltimer_ns() - t0 > 200000000ull) return;
-  }
-}
 
 // Mask of the 16-bit halves of `w` that are infinite or NaN.
 template <bool FP16>
@@ -203,9 +95,9 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
       tma_prefetch_desc(&tk);
       tma_prefetch_desc(&tv);
     }
-    const int64_t total = total_work<NX>(p, lane, blockIdx.x == 0);
+    const int64_t total = total_work<kTile * NX>(p.cache, p.tok, lane, blockIdx.x == 0);
     const int64_t a = run_start(total, blockIdx.x, gridDim.x), z = run_start(total, blockIdx.x + 1, gridDim.x);
-    const RunStart r = z > a ? find_start<NX>(p, a, static_cast<int>(z - a), lane) : RunStart{0, 0, 0, 0};
+    const RunStart r = z > a ? find_start<kTile * NX>(p.cache, p.tok, a, static_cast<int>(z - a), lane) : RunStart{0, 0, 0, 0};
     if (lane == 0) *run_sm = r;
   }
   if (warp == 1) {
@@ -229,19 +121,12 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
   if (wd.aborted()) {
   } else if (warp == 0) {
     // ------------------------------------------------------------ producer
-    Walk<NX> w(p, run);
+    Walk<kTile * NX> w(p.cache, p.tok, run);
     uint32_t kv = 0;
     bool stop = false;
     const int boxes = kTile >> p.box_log;
-    // the page of this lane's box of key tile `t`: n_pages (a page past the end) for a box of no slot in use
-    auto page_for = [&](int t) -> int {
-      const int s = t * kTile + (lane << p.box_log);
-      if (lane >= boxes || s >= w.s.len + w.s.n) return p.cache.n_pages;
-      const int pg = page_of(p.cache, w.b, s);
-      if (pg < 0) record_status(p.cache.status, BSA_ERR_BAD_CACHE);
-      return pg < 0 ? p.cache.n_pages : pg;
-    };
-    while (!stop && w.next(p)) {
+    auto page_for = [&](int t) { return box_page(p.cache, w, t, lane << p.box_log); };
+    while (!stop && w.next(p.cache, p.tok)) {
       int page_next = page_for(w.t0);
       for (int t = w.t0; t < w.t1; ++t, ++kv) {
         const int page = page_next;
@@ -282,7 +167,7 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      Walk<NX> w(p, run);
+      Walk<kTile * NX> w(p.cache, p.tok, run);
       uint32_t kv = 0;  // key tiles done
       bool stop = false;
       // S = Q_x K^T of key tile number i into S buffer `buf`
@@ -311,7 +196,7 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
         mma_commit(&bars[L::bPVDone + x]);
         return true;
       };
-      while (!stop && w.next(p)) {
+      while (!stop && w.next(p.cache, p.tok)) {
         const int nt = w.t1 - w.t0;
         for (int x = 0; x < NX && !stop; ++x) {
           if (!wd.wait(&bars[L::bQFull + x], w.index & 1)) stop = true;
@@ -355,10 +240,10 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
     auto wwait = [&](uint64_t *bar, uint32_t parity) {
       return __all_sync(0xffffffffu, wd.wait(bar, parity)) != 0;
     };
-    Walk<NX> w(p, run);
+    Walk<kTile * NX> w(p.cache, p.tok, run);
     uint32_t kv = 0;
     bool stop = false;
-    while (!stop && w.next(p)) {
+    while (!stop && w.next(p.cache, p.tok)) {
       const int row0 = (w.rg * NX + x) * kTile, rows = min(w.s.n * G - row0, kTile);
       const int row = row0 + r, tok = row / G, h = w.hk * G + row % G;
       const bool row_ok = r < rows, warp_on = quarter * 32 < rows;
@@ -590,13 +475,13 @@ __global__ void __launch_bounds__(256) k_attend_join(const AttendParams p, int c
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const int64_t rows = static_cast<int64_t>(p.cache.B) * p.tok.T * p.tok.H;
-  const int64_t total = total_work<NX>(p, lane, false);
+  const int64_t total = total_work<kTile * NX>(p.cache, p.tok, lane, false);
   bool waited = false;
   for (int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; i < rows;
        i += static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5)) {
     const int h = static_cast<int>(i % p.tok.H), t = static_cast<int>(i / p.tok.H % p.tok.T);
     const int b = static_cast<int>(i / p.tok.H / p.tok.T);
-    const Seq<NX> s = sequence<NX>(p.cache, p.tok, b, false);
+    const Seq<kTile * NX> s = sequence<kTile * NX>(p.cache, p.tok, b, false);
     uint16_t *orow = p.out + b * p.os[0] + t * p.os[1] + h * p.os[2] + lane * E;
     float *lse = p.lse + (static_cast<int64_t>(b) * p.tok.H + h) * p.tok.T + t;
     if (t >= s.n) {
@@ -608,7 +493,7 @@ __global__ void __launch_bounds__(256) k_attend_join(const AttendParams p, int c
     // this row's item in the list: [a, a + tiles)
     int64_t a = 0;
     for (int b0 = 0; b0 < b; b0 += 32)
-      if (b0 + lane < b) a += sequence<NX>(p.cache, p.tok, b0 + lane, false).work(p.cache.H_kv);
+      if (b0 + lane < b) a += sequence<kTile * NX>(p.cache, p.tok, b0 + lane, false).work(p.cache.H_kv);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
     const int hk = h / p.tok.G, row = t * p.tok.G + h % p.tok.G, rg = row / (kTile * NX);

@@ -332,7 +332,12 @@ bsa_status bsa_cache_weigh(const bsa_cache *cache, const bsa_tokens *tok, const 
   a.score_in = score_in;
   a.score_out = score_out;
   a.scale = t.t.scale;
-  return of_cuda(launch_weigh(a, t.t.dtype == BSA_DTYPE_FP16, reinterpret_cast<cudaStream_t>(stream)));
+  const bool fp16 = t.t.dtype == BSA_DTYPE_FP16;
+  CUtensorMap tk;
+  if (!make_cache_map(&tk, c.k, c.n_pages, 1 << c.page_log, c.H_kv, c.D, c.ks, fp16)) return BSA_ERR_UNSUPPORTED;
+  int sms = 0;
+  if (!sm_count(&sms)) return BSA_ERR_NO_DEVICE;
+  return of_cuda(launch_weigh(a, tk, fp16, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 bsa_status bsa_cache_evict(const bsa_cache *cache, const bsa_evict_spec *e, void *ws, size_t ws_bytes,

@@ -112,7 +112,7 @@ struct WeighArgs {
   float *score_out;
   float scale;
 };
-cudaError_t launch_weigh(const WeighArgs &a, bool fp16, cudaStream_t s);
+cudaError_t launch_weigh(const WeighArgs &a, const CUtensorMap &tk, bool fp16, int sms, cudaStream_t s);
 
 struct EvictArgs {
   CacheView cache;
