@@ -16,12 +16,15 @@
 //               each (lane i looks up and loads box i); a box of no slot in use,
 //               and a page index out of range, reads a page past the end: zeros.
 //   warp 1      tcgen05 issuer, one lane: S = Q K^T (SS), O += P V (TS, P over
-//               the S columns).  NX = 1: the S of tile j+1 is computed under the
-//               softmax of tile j (two S buffers); NX = 2: the two row tiles
-//               alternate.
-//   warps 4-7, 8-11   softmax of row tile x, one row a thread: Q into shared
-//               memory, the tile's maximum, lazy rescale of O, P as 16-bit, the
-//               epilogue.  Tiles with new tokens are masked by the tree word.
+//               the S columns).
+//   warps 4-7, 8-11   two softmax groups, one row a thread with its 128 scores in
+//               registers (224 a thread, from the other warps' share): the tile's
+//               maximum, lazy rescale of O, P as 16-bit.  NX = 1: the groups take
+//               the key tiles in turn, each with its own running maximum, sums and
+//               O, and add the two up in the epilogue, each for half the columns
+//               (one group alone left the tensor and load pipes waiting for its
+//               chain of latencies: 187 -> 141 us, 16 sequences x 32 tokens x 4
+//               heads a group over 33002 keys).  NX = 2: a group a row tile.
 // V of what no row may see: slots past the new tokens are zeroed in shared memory
 // (0 * NaN is NaN in the product), and a new token's infinities and NaN are taken
 // out of the tile and added back in the epilogue of the rows that see the token.
@@ -54,7 +57,7 @@ struct AttendSmem {
   static constexpr int NK = D == 128 ? 3 : 5, NV = D == 128 ? (NX == 1 ? 3 : 2) : 5;
   static constexpr int kQ = 0, kK = NX * kTB, kV = kK + NK * kTB, kBar = kV + NV * kTB;
   static constexpr int bKFull = 0, bKEmpty = NK, bVFull = 2 * NK, bVEmpty = bVFull + NV, bQFull = bVEmpty + NV,
-                       bSFull = bQFull + NX, bPFull = bSFull + 2, bPVDone = bPFull + 2, bFinal = bPVDone + NX,
+                       bSFull = bQFull + NX, bPFull = bSFull + 2, bPVDone = bPFull + 2, bFinal = bPVDone + 2,
                        kNumBars = bFinal + 1;
   static constexpr int kBad = kBar + kNumBars * 8;     // uint32 [4][2]: new tokens whose V is not finite
   static constexpr int kRun = kBad + 32;               // RunStart
@@ -70,7 +73,7 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
 }
 
 template <bool FP16, int D, int NX>
-__global__ void __launch_bounds__(NX == 1 ? 256 : 384, 1)
+__global__ void __launch_bounds__(384, 1)
 k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttendParams p) {
   using L = AttendSmem<D, NX>;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -84,7 +87,7 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
 
   if (threadIdx.x == 32) {
     for (int i = 0; i < L::kNumBars; ++i)
-      mbar_init(&bars[i], (i >= L::bQFull && i < L::bQFull + NX) || (i >= L::bPFull && i < L::bPFull + 2) ? 128 : 1);
+      mbar_init(&bars[i], i >= L::bQFull && i < L::bQFull + NX ? 256 / NX : i >= L::bPFull && i < L::bPFull + 2 ? 128 : 1);
     *abort_flag = 0;
     for (int i = 0; i < 8; ++i) bad[i] = 0;
     fence_mbar_init();
@@ -95,9 +98,7 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
       tma_prefetch_desc(&tk);
       tma_prefetch_desc(&tv);
     }
-    const int64_t total = total_work<kTile * NX>(p.cache, p.tok, lane, blockIdx.x == 0);
-    const int64_t a = run_start(total, blockIdx.x, gridDim.x), z = run_start(total, blockIdx.x + 1, gridDim.x);
-    const RunStart r = z > a ? find_start<kTile * NX>(p.cache, p.tok, a, static_cast<int>(z - a), lane) : RunStart{0, 0, 0, 0};
+    const RunStart r = find_run<kTile * NX>(p.cache, p.tok, lane);
     if (lane == 0) *run_sm = r;
   }
   if (warp == 1) {
@@ -118,6 +119,9 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
   constexpr uint32_t kIdescS = FP16 ? idesc_f16_f32(128, 128, 0, 0) : idesc_bf16_f32(128, 128, 0, 0);
   constexpr uint32_t kIdescPV = FP16 ? idesc_f16_f32(128, D, 0, 1) : idesc_bf16_f32(128, D, 0, 1);
 
+  // the launch's 384 x 168 registers: 128 x 56 + 256 x 224
+  if (warp < 4) {
+  regs_dec<56>();
   if (wd.aborted()) {
   } else if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -168,83 +172,93 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       Walk<kTile * NX> w(p.cache, p.tok, run);
-      uint32_t kv = 0;  // key tiles done
+      uint32_t kv = 0, used[2] = {0, 0};  // key tiles done; tiles each group has had
       bool stop = false;
-      // S = Q_x K^T of key tile number i into S buffer `buf`
-      auto issue_s = [&](int x, int buf, uint32_t i) -> bool {
+      // S_x = Q K^T of key tile number i for group x
+      auto issue_s = [&](int x, uint32_t i) -> bool {
         if (!wd.wait(&bars[L::bKFull + i % NK], (i / NK) & 1)) return false;
         tc_fence_after();
-        const uint32_t q_addr = smem_u32(sm + L::kQ + x * kTB), k_addr = smem_u32(sm + L::kK + (i % NK) * kTB);
+        const uint32_t q_addr = smem_u32(sm + L::kQ + (NX == 1 ? 0 : x) * kTB);
+        const uint32_t k_addr = smem_u32(sm + L::kK + (i % NK) * kTB);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-          mma_ss(tmem + buf * 128, sw128_desc(q_addr + off, 16, 1024), sw128_desc(k_addr + off, 16, 1024), kIdescS,
+          mma_ss(tmem + x * 128, sw128_desc(q_addr + off, 16, 1024), sw128_desc(k_addr + off, 16, 1024), kIdescS,
                  kk > 0);
         }
-        mma_commit(&bars[L::bSFull + buf]);
+        mma_commit(&bars[L::bSFull + x]);
         return true;
       };
-      // O_x += P V of key tile number i, P in S buffer `buf`
-      auto issue_pv = [&](int x, int buf, uint32_t i, bool first) -> bool {
-        if (!wd.wait(&bars[L::bPFull + buf], (NX == 1 ? i >> 1 : i) & 1)) return false;
+      // O_x += P_x V of key tile number i
+      auto issue_pv = [&](int x, uint32_t i, bool first) -> bool {
+        if (!wd.wait(&bars[L::bPFull + x], used[x] & 1)) return false;
+        ++used[x];
         tc_fence_after();
         const uint32_t v_addr = smem_u32(sm + L::kV + (i % NV) * kTB);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + 256 + x * D, tmem + buf * 128 + kk * 8, sw128_desc(v_addr + kk * 2048, 16384, 1024), kIdescPV,
+          mma_ts(tmem + 256 + x * D, tmem + x * 128 + kk * 8, sw128_desc(v_addr + kk * 2048, 16384, 1024), kIdescPV,
                  (!first || kk > 0) ? 1u : 0u);
         mma_commit(&bars[L::bPVDone + x]);
         return true;
       };
       while (!stop && w.next(p.cache, p.tok)) {
         const int nt = w.t1 - w.t0;
-        for (int x = 0; x < NX && !stop; ++x) {
-          if (!wd.wait(&bars[L::bQFull + x], w.index & 1)) stop = true;
-          tc_fence_after();
-          if (!stop && !issue_s(x, NX == 1 ? kv & 1 : x, kv)) stop = true;
-        }
+        for (int x = 0; x < NX && !stop; ++x) stop = !wd.wait(&bars[L::bQFull + x], w.index & 1);
         if (stop) break;
-        mma_commit(&bars[L::bKEmpty + kv % NK]);
-        for (int j = 0; j < nt; ++j, ++kv) {
-          const bool more = j + 1 < nt;
-          if constexpr (NX == 1) {
-            // the other S buffer: its P (tile kv - 1) is read by MMAs issued before
-            if (more) {
-              if (!issue_s(0, (kv + 1) & 1, kv + 1)) { stop = true; break; }
-              mma_commit(&bars[L::bKEmpty + (kv + 1) % NK]);
+        tc_fence_after();
+        // an S follows the PV that reads P from its columns in issue order, so needs no wait for it
+        if constexpr (NX == 1) {
+          for (int j = 0; j < min(nt, 2) && !stop; ++j) {
+            stop = !issue_s((kv + j) & 1, kv + j);
+            if (!stop) mma_commit(&bars[L::bKEmpty + (kv + j) % NK]);
+          }
+          for (int j = 0; j < nt && !stop; ++j, ++kv) {
+            if (!wd.wait(&bars[L::bVFull + kv % NV], (kv / NV) & 1)) { stop = true; break; }
+            if (!issue_pv(kv & 1, kv, j < 2)) { stop = true; break; }
+            mma_commit(&bars[L::bVEmpty + kv % NV]);
+            if (j + 2 < nt) {
+              if (!issue_s(kv & 1, kv + 2)) { stop = true; break; }
+              mma_commit(&bars[L::bKEmpty + (kv + 2) % NK]);
             }
+          }
+        } else {
+          for (int x = 0; x < 2 && !stop; ++x) stop = !issue_s(x, kv);
+          if (stop) break;
+          mma_commit(&bars[L::bKEmpty + kv % NK]);
+          for (int j = 0; j < nt && !stop; ++j, ++kv) {
             if (!wd.wait(&bars[L::bVFull + kv % NV], (kv / NV) & 1)) { stop = true; break; }
-            if (!issue_pv(0, kv & 1, kv, j == 0)) { stop = true; break; }
-          } else {
-            if (!wd.wait(&bars[L::bVFull + kv % NV], (kv / NV) & 1)) { stop = true; break; }
-            for (int x = 0; x < NX; ++x) {
-              if (!issue_pv(x, x, kv, j == 0)) { stop = true; break; }
-              if (more && !issue_s(x, x, kv + 1)) { stop = true; break; }
+            for (int x = 0; x < 2 && !stop; ++x) {
+              stop = !issue_pv(x, kv, j == 0);
+              if (!stop && j + 1 < nt) stop = !issue_s(x, kv + 1);
             }
             if (stop) break;
-            if (more) mma_commit(&bars[L::bKEmpty + (kv + 1) % NK]);
+            mma_commit(&bars[L::bVEmpty + kv % NV]);
+            if (j + 1 < nt) mma_commit(&bars[L::bKEmpty + (kv + 1) % NK]);
           }
-          mma_commit(&bars[L::bVEmpty + kv % NV]);
         }
       }
       mma_commit(&bars[L::bFinal]);
       drain_wait(&bars[L::bFinal], 0);
     }
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------ softmax of row tile x
+  }
+  } else {
+    // ------------------------------------------------------------ softmax group x
+    regs_inc<224>();
     const int x = (warp - 4) >> 2;
     const int quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t t_o = tmem + lane_off + 256 + x * D;
+    const uint32_t t_s = tmem + lane_off + x * 128, t_o = tmem + lane_off + 256 + x * D;
     const int G = p.tok.G;
+    constexpr int kPieces = D / 8;
     auto wwait = [&](uint64_t *bar, uint32_t parity) {
       return __all_sync(0xffffffffu, wd.wait(bar, parity)) != 0;
     };
     Walk<kTile * NX> w(p.cache, p.tok, run);
-    uint32_t kv = 0;
-    bool stop = false;
-    while (!stop && w.next(p.cache, p.tok)) {
-      const int row0 = (w.rg * NX + x) * kTile, rows = min(w.s.n * G - row0, kTile);
+    uint32_t kv = 0, used = 0;  // key tiles of the run so far, and this group's among them
+    bool stop = wd.aborted();
+    while (w.next(p.cache, p.tok)) {
+      const int row0 = (w.rg * NX + (NX == 1 ? 0 : x)) * kTile, rows = min(w.s.n * G - row0, kTile);
       const int row = row0 + r, tok = row / G, h = w.hk * G + row % G;
       const bool row_ok = r < rows, warp_on = quarter * 32 < rows;
       uint32_t *bad_w = bad + (w.index & 3) * 2;
@@ -252,25 +266,22 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
         bad[((w.index + 1) & 3) * 2] = 0;
         bad[((w.index + 1) & 3) * 2 + 1] = 0;
       }
-      // Q rows -> shared memory (the last S of the piece before has read them), 16 bytes a lane
-      constexpr int kPieces = D / 8;
+      // Q rows -> shared memory (every S of the piece before has read them), 16 bytes a lane
 #pragma unroll 4
-      for (int i = r; i < kTile * kPieces; i += kTile) {
+      for (int i = NX == 1 ? threadIdx.x - 128 : r; i < rows * kPieces; i += 256 / NX) {
         const int rr = i / kPieces, c = i % kPieces, grow = row0 + rr;
-        if (rr < rows) {
-          const int4 v = *reinterpret_cast<const int4 *>(p.q + w.b * p.qs[0] + (grow / G) * p.qs[1] +
-                                                         (w.hk * G + grow % G) * p.qs[2] + c * 8);
-          *reinterpret_cast<int4 *>(sm + L::kQ + x * kTB + (c >> 3) * 16384 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v;
-        }
+        const int4 v = *reinterpret_cast<const int4 *>(p.q + w.b * p.qs[0] + (grow / G) * p.qs[1] +
+                                                       (w.hk * G + grow % G) * p.qs[2] + c * 8);
+        *reinterpret_cast<int4 *>(sm + L::kQ + (NX == 1 ? 0 : x) * kTB + (c >> 3) * 16384 + rr * 128 +
+                                  (((c & 7) ^ (rr & 7)) << 4)) = v;
       }
       fence_proxy_async_smem();
-      mbar_arrive(&bars[L::bQFull + x]);
+      mbar_arrive(&bars[L::bQFull + (NX == 1 ? 0 : x)]);
       const uint64_t word = row_ok ? tree_word(p.tok, w.b, tok, w.s.n) : 0ull;
       float m_ref = -INFINITY, l = 0.f, l_r = 0.f;
 
-      for (int t = w.t0; t < w.t1; ++t, ++kv) {
-        const int buf = NX == 1 ? kv & 1 : x;
-        const uint32_t t_s = tmem + lane_off + buf * 128;
+      for (int t = w.t0; t < w.t1 && !stop; ++t, ++kv) {
+        if (NX == 1 && (kv & 1) != static_cast<uint32_t>(x)) continue;
         const int j0 = t * kTile;
         const bool edge = j0 + kTile > w.s.len;
         uint32_t allow[4] = {~0u, ~0u, ~0u, ~0u};
@@ -282,7 +293,7 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
             else if (d0 >= 0) allow[q] = static_cast<uint32_t>(word >> d0);
             else if (d0 > -32) allow[q] = static_cast<uint32_t>(word << -d0) | ((1u << -d0) - 1u);
           }
-          if (x == 0) {
+          if (NX == 1 || x == 0) {
             // this thread's key: V past the new tokens becomes zero, what is not
             // finite in a new token's V is taken out
             if (!wwait(&bars[L::bVFull + kv % NV], (kv / NV) & 1)) { stop = true; break; }
@@ -307,27 +318,29 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
               if (found) atomicOr(bad_w + (d >> 5), 1u << (d & 31));
               fence_proxy_async_smem();
             }
+            __syncwarp();
           }
         }
-        if (!wwait(&bars[L::bSFull + buf], (NX == 1 ? kv >> 1 : kv) & 1)) { stop = true; break; }
+        if (!wwait(&bars[L::bSFull + x], used & 1)) { stop = true; break; }
         tc_fence_after();
         if (warp_on) {
-          float mx = -INFINITY;
+          uint32_t sv[4][32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t sv[32];
-            tmem_ld32(t_s + 32 * c, sv);
-            tmem_wait_ld();
-            if (edge) {
+          for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, sv[c]);
+          tmem_wait_ld();
+          if (edge) {
+            // what this row does not see, whatever it holds
 #pragma unroll
-              for (int q = 0; q < 32; ++q)
-                mx = fmaxf(mx, ((allow[c] >> q) & 1u) ? __uint_as_float(sv[q]) : -INFINITY);
-            } else {
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int q = 0; q < 32; ++q) mx = fmaxf(mx, __uint_as_float(sv[q]));
-            }
+              for (int q = 0; q < 32; ++q) sv[c][q] = ((allow[c] >> q) & 1u) ? sv[c][q] : 0xff800000u;
           }
-          const float mt = mx * p.scale_log2;
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int q = 0; q < 32; ++q)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) mx4[c] = fmaxf(mx4[c], __uint_as_float(sv[c][q]));
+          const float mt = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
           const bool need = mt > m_ref + kRescaleThreshold;
           const bool resc = need && l > 0.f;
           float alpha = 1.f;
@@ -338,18 +351,18 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
             m_ref = mt;
           }
           if (__any_sync(0xffffffffu, resc)) {
-            // every PV so far is in O (resc: this piece has had one)
-            if (!wwait(&bars[L::bPVDone + x], (kv - 1) & 1)) { stop = true; break; }
+            // every PV of this group so far is in O (resc: this piece has had one)
+            if (!wwait(&bars[L::bPVDone + x], (used - 1) & 1)) { stop = true; break; }
             tc_fence_after();
             const float a = resc ? alpha : 1.f;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(t_o + c * 32, o);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(t_o + c * 16, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * a);
-              tmem_st32(t_o + c * 32, o);
+              for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * a);
+              tmem_st16(t_o + c * 16, o);
             }
             tmem_wait_st();
           }
@@ -358,60 +371,89 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
           // denominator carry the same rounding)
           const float mu = m_ref == -INFINITY ? 0.f : m_ref;
           const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nmu = make_float2(-mu, -mu);
-          float2 rs2 = make_float2(0.f, 0.f), rr2 = make_float2(0.f, 0.f);
-          uint32_t svb[2][16];
-          tmem_ld16(t_s, svb[0]);
-          tmem_wait_ld();
+          float2 rs2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, rr2[2] = {rs2[0], rs2[0]};
 #pragma unroll
-          for (int sc = 0; sc < 8; ++sc) {
-            if (sc + 1 < 8) tmem_ld16(t_s + 16 * (sc + 1), svb[(sc + 1) & 1]);
-            const uint32_t *sv = svb[sc & 1];
-            const uint32_t bits = allow[sc >> 1] >> (16 * (sc & 1));
-            uint32_t pk[8];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float2 e = __ffma2_rn(make_float2(__uint_as_float(sv[2 * q]), __uint_as_float(sv[2 * q + 1])), sc2, nmu);
-              float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
-              if (edge) {
-                p0 = ((bits >> (2 * q)) & 1u) ? p0 : 0.f;
-                p1 = ((bits >> (2 * q + 1)) & 1u) ? p1 : 0.f;
-              }
-              pk[q] = pack16<FP16>(p0, p1);
-              rs2 = __fadd2_rn(rs2, make_float2(p0, p1));
-              rr2 = __fadd2_rn(rr2, unpack16<FP16>(pk[q]));
+            for (int q = 0; q < 16; ++q) {
+              const float2 e =
+                  __ffma2_rn(make_float2(__uint_as_float(sv[c][2 * q]), __uint_as_float(sv[c][2 * q + 1])), sc2, nmu);
+              const float2 pp = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+              pk[q] = pack16<FP16>(pp.x, pp.y);
+              rs2[q & 1] = __fadd2_rn(rs2[q & 1], pp);
+              rr2[q & 1] = __fadd2_rn(rr2[q & 1], unpack16<FP16>(pk[q]));
             }
-            tmem_st8(t_s + 8 * sc, pk);
-            if (sc + 1 < 8) tmem_wait_ld();
+            tmem_st16(t_s + 16 * c, pk);
           }
-          l += rs2.x + rs2.y;
-          l_r += rr2.x + rr2.y;
+          l += (rs2[0].x + rs2[1].x) + (rs2[0].y + rs2[1].y);
+          l_r += (rr2[0].x + rr2[1].x) + (rr2[0].y + rr2[1].y);
           tmem_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(&bars[L::bPFull + buf]);
+        mbar_arrive(&bars[L::bPFull + x]);
+        ++used;
       }
-      if (stop) break;
       // ---------------------------------------------------------- epilogue
-      // NX = 1 issues S of the last tile before the PV of the one before it, so that PV may still run: its phase
-      // first (a wait two phases ahead would pass at once)
-      if (NX == 1 && w.t1 - w.t0 > 1 && !wwait(&bars[L::bPVDone + x], kv & 1)) break;
-      if (!wwait(&bars[L::bPVDone + x], (kv - 1) & 1)) break;
+      // (a group that has had no tile in the piece has nothing to wait for)
+      const bool had = NX == 2 || w.t1 - w.t0 > 1 || ((kv - 1) & 1) == static_cast<uint32_t>(x);
+      if (!stop && had && !wwait(&bars[L::bPVDone + x], (used - 1) & 1)) stop = true;
       tc_fence_after();
-      if (warp_on) {
+      float f_mine = 1.f, f_other = 0.f;
+      const bool both = NX == 1 && w.t1 - w.t0 > 1;
+      if constexpr (NX == 1) {
+        // the other group's maximum and sums, through this row's TMEM lane (its S columns are free)
+        if (!stop && both) {
+          uint32_t mine[8] = {__float_as_uint(m_ref), __float_as_uint(l), __float_as_uint(l_r), 0, 0, 0, 0, 0};
+          tmem_st8(t_s, mine);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        named_bar_sync(1, 256);  // in every path, so that the two groups' barriers pair up
+        tc_fence_after();
+        if (!stop && both) {
+          uint32_t other[16];
+          tmem_ld16(tmem + lane_off + (x ^ 1) * 128, other);
+          tmem_wait_ld();
+          const float mo = __uint_as_float(other[0]), M = fmaxf(m_ref, mo), Mu = M == -INFINITY ? 0.f : M;
+          f_mine = exp2f(m_ref - Mu);
+          f_other = exp2f(mo - Mu);
+          l = f_mine * l + f_other * __uint_as_float(other[1]);
+          l_r = f_mine * l_r + f_other * __uint_as_float(other[2]);
+          m_ref = M;
+        } else if (!had) {
+          // the piece's one tile was the other group's, which writes the rows
+        }
+      }
+      if (!stop && warp_on && had) {
         const uint32_t bad_lo = bad_w[0] & static_cast<uint32_t>(word), bad_hi = bad_w[1] & static_cast<uint32_t>(word >> 32);
         const bool any_bad = __any_sync(0xffffffffu, (bad_lo | bad_hi) != 0u);
         const float inv = w.whole ? (l_r > 0.f ? 1.f / l_r : 0.f) : 1.f;
+        f_mine *= inv;
+        f_other *= inv;
         uint16_t *orow = p.out + w.b * p.os[0] + tok * p.os[1] + h * p.os[2];
         // a piece that starts this CTA's run goes to slot 0, one that ends it to slot 1
-        const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (w.index > 0 ? 1 : 0)) * (kTile * NX) + x * kTile + r;
+        const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (w.index > 0 ? 1 : 0)) * (kTile * NX) +
+                             (NX == 1 ? 0 : x) * kTile + r;
         float *prow = p.part_o + part * D;
-        uint32_t ob[2][16];
-        tmem_ld16(t_o, ob[0]);
-        tmem_wait_ld();
+        // the columns [c0, c1) * 16: half of them where both groups hold a part of the row
+        const int c0 = both ? x * (D / 32) : 0, c1 = both ? c0 + D / 32 : D / 16;
+#pragma unroll 1
+        for (int c = c0; c < c1; ++c) {
+          uint32_t o[16];
+          tmem_ld16(t_o + c * 16, o);
+          if (both) {
+            uint32_t o2[16];
+            tmem_ld16(tmem + lane_off + 256 + (x ^ 1) * D + c * 16, o2);
+            tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          if (c + 1 < D / 16) tmem_ld16(t_o + (c + 1) * 16, ob[(c + 1) & 1]);
-          uint32_t *o = ob[c & 1];
+            for (int q = 0; q < 16; ++q)
+              o[q] = __float_as_uint(__uint_as_float(o[q]) * f_mine + __uint_as_float(o2[q]) * f_other);
+          } else {
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f_mine);
+          }
           if (any_bad) {
             // the seen tokens' infinities and NaN, in this row's 16 columns
             for (uint64_t todo = bad_lo | static_cast<uint64_t>(bad_hi) << 32; todo != 0ull; todo &= todo - 1) {
@@ -434,7 +476,7 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
               uint32_t wv[8];
 #pragma unroll
               for (int q = 0; q < 8; ++q)
-                wv[q] = pack16<FP16>(__uint_as_float(o[2 * q]) * inv, __uint_as_float(o[2 * q + 1]) * inv);
+                wv[q] = pack16<FP16>(__uint_as_float(o[2 * q]), __uint_as_float(o[2 * q + 1]));
               int4 *dst = reinterpret_cast<int4 *>(orow + c * 16);
               dst[0] = make_int4(wv[0], wv[1], wv[2], wv[3]);
               dst[1] = make_int4(wv[4], wv[5], wv[6], wv[7]);
@@ -445,15 +487,17 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
               st_global_v8(prow + c * 16 + 8, hi);
             }
           }
-          if (c + 1 < D / 16) tmem_wait_ld();
+          __syncwarp();
         }
-        tc_fence_before();
-        if (row_ok) {
+        if (row_ok && !(both && x == 1)) {
           if (w.whole) p.lse[(static_cast<int64_t>(w.b) * p.tok.H + h) * p.tok.T + tok] =
               l == 0.f ? -INFINITY : (m_ref + __log2f(l)) * kLn2;
           else p.part_ml[part] = make_float4(m_ref, l, l_r, 0.f);
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (stop) break;
     }
   }
 
@@ -465,87 +509,108 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
   }
 }
 
-// Joins the pieces of the rows whose key tiles several runs share, one warp a
-// row, the pieces in tile order:
+// Joins the pieces of the rows whose key tiles several runs share, the pieces in
+// tile order:
 //   M = max m_i, O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) lr_i,
 //   LSE = (M + log2 sum 2^(m_i - M) l_i) ln 2.
-// Rows at or past n_new are written as 0 / -inf here.
-template <bool FP16, int D, int NX>
+// A row is WARPS warps of a block, which share out its pieces (a long sequence
+// alone on the GPU is in up to 148) and add their parts up in order, so the same
+// lengths give the same bits.  Rows at or past n_new are written as 0 / -inf here.
+template <bool FP16, int D, int NX, int WARPS>
 __global__ void __launch_bounds__(256) k_attend_join(const AttendParams p, int ctas) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
+  constexpr int E = D / 32, kRowsPerBlock = 8 / WARPS;
+  __shared__ float part_sm[WARPS > 1 ? 8 : 1][D + 4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WARPS;
   const int64_t rows = static_cast<int64_t>(p.cache.B) * p.tok.T * p.tok.H;
-  const int64_t total = total_work<kTile * NX>(p.cache, p.tok, lane, false);
-  bool waited = false;
-  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; i < rows;
-       i += static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5)) {
-    const int h = static_cast<int>(i % p.tok.H), t = static_cast<int>(i / p.tok.H % p.tok.T);
-    const int b = static_cast<int>(i / p.tok.H / p.tok.T);
-    const Seq<kTile * NX> s = sequence<kTile * NX>(p.cache, p.tok, b, false);
-    uint16_t *orow = p.out + b * p.os[0] + t * p.os[1] + h * p.os[2] + lane * E;
-    float *lse = p.lse + (static_cast<int64_t>(b) * p.tok.H + h) * p.tok.T + t;
-    if (t >= s.n) {
-#pragma unroll
-      for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(orow + e) = 0u;
-      if (lane == 0) *lse = -INFINITY;
-      continue;
-    }
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRowsPerBlock + warp / WARPS;
+  const bool in = i < rows;
+  const int h = in ? static_cast<int>(i % p.tok.H) : 0, t = in ? static_cast<int>(i / p.tok.H % p.tok.T) : 0;
+  const int b = in ? static_cast<int>(i / p.tok.H / p.tok.T) : 0;
+  uint32_t a;
+  const Runs runs(total_work<kTile * NX>(p.cache, p.tok, lane, false, b, &a), ctas);
+  const Seq<kTile * NX> s = sequence<kTile * NX>(p.cache, p.tok, b, false);
+  uint16_t *orow = p.out + b * p.os[0] + t * p.os[1] + h * p.os[2] + lane * E;
+  float *lse = p.lse + (static_cast<int64_t>(b) * p.tok.H + h) * p.tok.T + t;
+  const bool padding = t >= s.n;
+  uint32_t c0 = 0, c1 = 0;
+  int64_t row_part = 0;
+  if (in && !padding) {
     // this row's item in the list: [a, a + tiles)
-    int64_t a = 0;
-    for (int b0 = 0; b0 < b; b0 += 32)
-      if (b0 + lane < b) a += sequence<kTile * NX>(p.cache, p.tok, b0 + lane, false).work(p.cache.H_kv);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
     const int hk = h / p.tok.G, row = t * p.tok.G + h % p.tok.G, rg = row / (kTile * NX);
-    a += (static_cast<int64_t>(hk) * s.groups + rg) * s.tiles;
-    // the run that holds list position x: the largest c with total c / ctas <= x
-    auto run_of = [&](int64_t x) {
-      int c = static_cast<int>(((x + 1) * ctas - 1) / total);
-      return min(c, ctas - 1);
+    a += (static_cast<uint32_t>(hk) * s.groups + rg) * s.tiles;
+    c0 = runs.of(a);
+    c1 = runs.of(a + s.tiles - 1);
+    row_part = row - rg * kTile * NX;
+  }
+  const bool joined = c0 != c1;  // else one run has written the row
+  // a grid that ends before the one it depends on would let the next kernel of the
+  // stream start early, so every warp waits
+  pdl_wait();
+  float M = -INFINITY, l = 0.f, l_r = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  if (joined) {
+    // the runs c0 .. c1 are not empty; c0's piece is its last, unless it starts there
+    auto part_of = [&](uint32_t c) {
+      const int slot = runs.start(c) >= a ? 0 : 1;
+      return (static_cast<int64_t>(c) * 2 + slot) * (kTile * NX) + row_part;
     };
-    const int c0 = run_of(a), c1 = run_of(a + s.tiles - 1);
-    if (c0 == c1) continue;  // one run did it all
-    if (!waited) {
-      pdl_wait();
-      waited = true;
-    }
-    const int in = row - rg * kTile * NX;
-    auto part_of = [&](int c) {
-      const int slot = run_start(total, c, ctas) >= a ? 0 : 1;
-      return (static_cast<int64_t>(c) * 2 + slot) * (kTile * NX) + in;
-    };
-    float M = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32)
-      if (run_start(total, c, ctas) < run_start(total, c + 1, ctas)) M = fmaxf(M, p.part_ml[part_of(c)].x);
+    for (uint32_t c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_ml[part_of(c)].x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
     const float Mu = M == -INFINITY ? 0.f : M;
-    float o[E], l = 0.f, l_r = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    const uint32_t n = c1 - c0 + 1, z = c0 + n * (sub + 1) / WARPS;
 #pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      if (run_start(total, c, ctas) >= run_start(total, c + 1, ctas)) continue;  // an empty run
+    for (uint32_t c = c0 + n * sub / WARPS; c < z; ++c) {
       const int64_t part = part_of(c);
       const float4 ml = p.part_ml[part];
       const float f = exp2f(ml.x - Mu);
       l = fmaf(f, ml.y, l);
       l_r = fmaf(f, ml.z, l_r);
       const float *src = p.part_o + part * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 v = *reinterpret_cast<const float2 *>(src + e);
-        o[e] = fmaf(f, v.x, o[e]);
-        o[e + 1] = fmaf(f, v.y, o[e + 1]);
+      if constexpr (E == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(src);
+        o[0] = fmaf(f, v.x, o[0]);
+        o[1] = fmaf(f, v.y, o[1]);
+        o[2] = fmaf(f, v.z, o[2]);
+        o[3] = fmaf(f, v.w, o[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2 *>(src);
+        o[0] = fmaf(f, v.x, o[0]);
+        o[1] = fmaf(f, v.y, o[1]);
       }
     }
-    const float inv = l_r > 0.f ? 1.f / l_r : 0.f;
-#pragma unroll
-    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(orow + e) = pack16<FP16>(o[e] * inv, o[e + 1] * inv);
-    if (lane == 0) *lse = l == 0.f ? -INFINITY : (M + __log2f(l)) * kLn2;
   }
-  // a grid that ends before the one it depends on would let the next kernel of the stream start early
-  if (!waited) pdl_wait();
+  if constexpr (WARPS > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) part_sm[warp][lane * E + e] = o[e];
+    if (lane == 0) {
+      part_sm[warp][D] = l;
+      part_sm[warp][D + 1] = l_r;
+    }
+    __syncthreads();
+    if (sub != 0) return;
+    for (int x = 1; x < WARPS; ++x) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += part_sm[warp + x][lane * E + e];
+      l += part_sm[warp + x][D];
+      l_r += part_sm[warp + x][D + 1];
+    }
+  }
+  if (!in || !(joined || padding)) return;
+  const float inv = l_r > 0.f ? 1.f / l_r : (l_r == 0.f ? 0.f : l_r);
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t *>(orow + e) = padding ? 0u : pack16<FP16>(o[e] * inv, o[e + 1] * inv);
+  if (lane == 0) *lse = l == 0.f ? -INFINITY : (M + __log2f(l)) * kLn2;
+}
+
+template <bool FP16, int D, int NX, int WARPS>
+cudaError_t join(const AttendParams &p, int ctas, cudaStream_t s) {
+  constexpr int kRowsPerBlock = 8 / WARPS;
+  const int64_t rows = static_cast<int64_t>(p.cache.B) * p.tok.T * p.tok.H;
+  return launch_pdl(k_attend_join<FP16, D, NX, WARPS>, dim3(static_cast<unsigned>((rows + kRowsPerBlock - 1) / kRowsPerBlock)),
+                    dim3(256), 0, s, p, ctas);
 }
 
 template <bool FP16, int D, int NX>
@@ -555,11 +620,11 @@ cudaError_t launch(const AttendParams &p, const CUtensorMap &tk, const CUtensorM
   cudaError_t e = cudaFuncSetAttribute(k_attend<FP16, D, NX>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
   if (e != cudaSuccess) return e;
   count_launch(2);
-  k_attend<FP16, D, NX><<<ctas, NX == 1 ? 256 : 384, L::kAlloc, s>>>(tk, tv, p);
+  k_attend<FP16, D, NX><<<ctas, 384, L::kAlloc, s>>>(tk, tv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int64_t rows = static_cast<int64_t>(p.cache.B) * p.tok.T * p.tok.H;
-  const int64_t blocks = std::min<int64_t>((rows + 7) / 8, 4 * ctas);
-  return launch_pdl(k_attend_join<FP16, D, NX>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, p, ctas);
+  // an item's tiles lie in about ctas / items runs, a few more where lengths differ
+  const int64_t items = static_cast<int64_t>(p.cache.B) * p.cache.H_kv * ((p.tok.T * p.tok.G + kTile * NX - 1) / (kTile * NX));
+  return ctas > 8 * items ? join<FP16, D, NX, 8>(p, ctas, s) : join<FP16, D, NX, 1>(p, ctas, s);
 }
 
 }  // namespace

@@ -15,7 +15,7 @@ constexpr int kAllRows = 0;
 template <int ROWS>
 struct Seq {
   int len, n, tiles, groups;
-  __device__ __forceinline__ int64_t work(int H_kv) const { return static_cast<int64_t>(H_kv) * groups * tiles; }
+  __device__ __forceinline__ uint32_t work(int H_kv) const { return static_cast<uint32_t>(H_kv) * groups * tiles; }
 };
 
 template <int ROWS>
@@ -28,43 +28,59 @@ __device__ __forceinline__ Seq<ROWS> sequence(const CacheView &c, const TokenVie
   return s;
 }
 
-__device__ __forceinline__ int64_t run_start(int64_t total, int cta, int ctas) { return total * cta / ctas; }
+// The list (fewer than 2^31 tiles) in `ctas` runs of one length, the first ones a
+// tile longer: run c is [start(c), start(c + 1)).
+struct Runs {
+  uint32_t total, base, rem;
+  __device__ __forceinline__ Runs(uint32_t total_, int ctas)
+      : total(total_), base(total_ / ctas), rem(total_ - base * ctas) {}
+  __device__ __forceinline__ uint32_t start(uint32_t c) const { return c * base + min(c, rem); }
+  // the run that holds list position x < total
+  __device__ __forceinline__ uint32_t of(uint32_t x) const {
+    const uint32_t longer = rem * (base + 1);
+    return x < longer ? x / (base + 1) : rem + (x - longer) / base;
+  }
+};
 
 struct RunStart {
   int b, item, tile, count;  // count: key tiles of the run
 };
 
-// Sum of work over the sequences, and the sequence that holds position `at`, by
-// one warp.
+// Length of the list, and of its part before sequence `upto`, by one warp.
 template <int ROWS>
-__device__ __forceinline__ int64_t total_work(const CacheView &c, const TokenView &t, int lane, bool report) {
-  int64_t sum = 0;
-  for (int b0 = 0; b0 < c.B; b0 += 32)
-    if (b0 + lane < c.B) sum += sequence<ROWS>(c, t, b0 + lane, report).work(c.H_kv);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  return sum;
+__device__ __forceinline__ uint32_t total_work(const CacheView &c, const TokenView &t, int lane, bool report, int upto,
+                                               uint32_t *before) {
+  uint32_t sum = 0, head = 0;
+  for (int b0 = 0; b0 < c.B; b0 += 32) {
+    const int b = b0 + lane;
+    const uint32_t w = b < c.B ? sequence<ROWS>(c, t, b, report).work(c.H_kv) : 0u;
+    sum += w;
+    head += b < upto ? w : 0u;
+  }
+  *before = __reduce_add_sync(0xffffffffu, head);
+  return __reduce_add_sync(0xffffffffu, sum);
 }
 
+// Where list position `at` lies, by one warp.
 template <int ROWS>
-__device__ __forceinline__ RunStart find_start(const CacheView &c, const TokenView &t, int64_t at, int count, int lane) {
+__device__ __forceinline__ RunStart find_start(const CacheView &c, const TokenView &t, uint32_t at, int count, int lane) {
   RunStart r{0, 0, 0, count};
-  int64_t base = 0;
+  uint32_t base = 0;
   for (int b0 = 0; b0 < c.B; b0 += 32) {
     Seq<ROWS> s{0, 0, 0, 0};
     if (b0 + lane < c.B) s = sequence<ROWS>(c, t, b0 + lane, false);
-    const int64_t w = s.work(c.H_kv);
-    int64_t incl = w;
+    const uint32_t w = s.work(c.H_kv);
+    uint32_t incl = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+      const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += o;
     }
-    const bool here = w > 0 && at >= base + incl - w && at < base + incl;
+    const uint32_t off = at - (base + incl - w);  // past w where `at` lies before this sequence too
+    const bool here = off < w;
     const uint32_t who = __ballot_sync(0xffffffffu, here);
     if (who != 0u) {
       const int src = __ffs(who) - 1;
-      const int64_t off = at - (base + incl - w);
       const int item = here ? static_cast<int>(off / s.tiles) : 0, tile = here ? static_cast<int>(off % s.tiles) : 0;
       r.b = b0 + src;
       r.item = __shfl_sync(0xffffffffu, item, src);
@@ -75,6 +91,15 @@ __device__ __forceinline__ RunStart find_start(const CacheView &c, const TokenVi
   }
   r.count = 0;
   return r;
+}
+
+// This CTA's run, by one warp.
+template <int ROWS>
+__device__ __forceinline__ RunStart find_run(const CacheView &c, const TokenView &t, int lane) {
+  uint32_t unused;
+  const Runs runs(total_work<ROWS>(c, t, lane, blockIdx.x == 0, 0, &unused), gridDim.x);
+  const uint32_t a = runs.start(blockIdx.x), z = runs.start(blockIdx.x + 1);
+  return z > a ? find_start<ROWS>(c, t, a, static_cast<int>(z - a), lane) : RunStart{0, 0, 0, 0};
 }
 
 // One CTA's run, piece by piece (a piece: consecutive key tiles of one item).

@@ -10,18 +10,25 @@
 //
 // One CTA per SM over an equal run of the (sequence, kv head, 128-key tile) list.
 //   warp 0      TMA producer of K tiles, one box a page (as in the attention).
-//   warp 1      tcgen05 issuer: S^T (128 keys x N rows, N <= 256) into one of two
-//               256-column TMEM buffers, alternating.
-//   warps 4-7, 8-11   the sums of the even and of the odd tiles; both load the
-//               rows (up to 256 at a time: more rows walk the piece's tiles again,
-//               adding to the same scores) and their -lse before a pass.
+//   warp 1      tcgen05 issuer: S^T (128 keys x up to 128 rows) into the TMEM
+//               buffer of the group whose tile it is.
+//   warps 4-19  four groups, each with every fourth tile and a 128-column buffer
+//               of its own (two groups on 256 columns, reading 16 columns at a
+//               time, left the exponential unit idle two thirds of the time: 137
+//               us against 105 at 4 x 16 tokens x 5 heads a group, 75600 keys).
+// Up to 256 rows are in shared memory, as two halves that a batch of four tiles
+// takes one after the other; more rows walk the piece's tiles again, adding to
+// the same scores.
 #include "runs.cuh"
 
 namespace bsa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kRows = 256;  // rows of one pass
+constexpr int kRows = 256;   // rows of one pass
+constexpr int kGroups = 4;   // groups of 128 threads, a thread a key
+constexpr int kSumThreads = kGroups * kTile;
+constexpr int kMaxTok = 64;
 
 struct WeighParams {
   CacheView cache;
@@ -37,24 +44,24 @@ struct WeighParams {
 template <int D>
 struct WeighSmem {
   static constexpr int kTB = kTile * D * 2;
-  static constexpr int NK = D == 128 ? 4 : 8;
+  static constexpr int NK = D == 128 ? 5 : 8;
   static constexpr int kQ = 0, kK = kRows * D * 2, kBar = kK + NK * kTB;
-  static constexpr int bKFull = 0, bKEmpty = NK, bSFull = 2 * NK, bSEmpty = bSFull + 2, bQFull = bSEmpty + 2,
+  static constexpr int bKFull = 0, bKEmpty = NK, bSFull = 2 * NK, bSEmpty = bSFull + kGroups, bQFull = bSEmpty + kGroups,
                        bFinal = bQFull + 1, kNumBars = bFinal + 1;
   static constexpr int kLse = kBar + ((kNumBars * 8 + 15) & ~15);  // float [kRows] -lse * log2e
-  static constexpr int kWord = kLse + kRows * 4;                    // uint32 [2][kRows] tree words, low and high
-  static constexpr int kRun = kWord + kRows * 8;
+  static constexpr int kWord = kLse + kRows * 4;                    // uint64 [kMaxTok] tree words
+  static constexpr int kRun = kWord + kMaxTok * 8;
   static constexpr int kMisc = kRun + 16;
   static constexpr int kAlloc = kMisc + 16;
 };
 
 template <bool FP16, int D>
-__global__ void __launch_bounds__(384, 1) k_weigh(const __grid_constant__ CUtensorMap tk, const WeighParams p) {
+__global__ void __launch_bounds__(128 + kSumThreads, 1) k_weigh(const __grid_constant__ CUtensorMap tk, const WeighParams p) {
   using L = WeighSmem<D>;
   extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::kBar);
   float *nlse = reinterpret_cast<float *>(sm + L::kLse);
-  uint32_t *words = reinterpret_cast<uint32_t *>(sm + L::kWord);
+  uint64_t *words = reinterpret_cast<uint64_t *>(sm + L::kWord);
   RunStart *run_sm = reinterpret_cast<RunStart *>(sm + L::kRun);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::kMisc);
   int *abort_flag = reinterpret_cast<int *>(sm + L::kMisc + 4);
@@ -62,16 +69,14 @@ __global__ void __launch_bounds__(384, 1) k_weigh(const __grid_constant__ CUtens
   constexpr int kTB = L::kTB, NK = L::NK;
 
   if (threadIdx.x == 32) {
-    for (int i = 0; i < L::kNumBars; ++i) mbar_init(&bars[i], i >= L::bSEmpty && i < L::bSEmpty + 2 ? 128 : 1);
+    for (int i = 0; i < L::kNumBars; ++i) mbar_init(&bars[i], i >= L::bSEmpty && i < L::bSEmpty + kGroups ? kTile : 1);
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
   if (warp == 0) {
     if (lane == 0) tma_prefetch_desc(&tk);
-    const int64_t total = total_work<kAllRows>(p.cache, p.tok, lane, blockIdx.x == 0);
-    const int64_t a = run_start(total, blockIdx.x, gridDim.x), z = run_start(total, blockIdx.x + 1, gridDim.x);
-    const RunStart r = z > a ? find_start<kAllRows>(p.cache, p.tok, a, static_cast<int>(z - a), lane) : RunStart{0, 0, 0, 0};
+    const RunStart r = find_run<kAllRows>(p.cache, p.tok, lane);
     if (lane == 0) *run_sm = r;
   }
   if (warp == 1) {
@@ -123,27 +128,38 @@ __global__ void __launch_bounds__(384, 1) k_weigh(const __grid_constant__ CUtens
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       Walk<kAllRows> w(p.cache, p.tok, run);
-      uint32_t kv = 0, loads = 0;
+      uint32_t kv = 0, loads = 0, ever = 0, odd = 0;  // bit y: buffer y has been used, an odd number of times
       bool stop = false;
       const uint32_t q_addr = smem_u32(sm + L::kQ);
       while (!stop && w.next(p.cache, p.tok)) {
         for (int pass = 0; pass < passes(w) && !stop; ++pass, ++loads) {
-          const int rows = min(w.s.n * G - pass * kRows, kRows), N = max((rows + 15) & ~15, 16);
-          const uint32_t idesc = FP16 ? idesc_f16_f32(128, N, 0, 0) : idesc_bf16_f32(128, N, 0, 0);
+          const int rows = min(w.s.n * G - pass * kRows, kRows), halves = rows > 128 ? 2 : 1;
           if (!wd.wait(&bars[L::bQFull], loads & 1)) { stop = true; break; }
           tc_fence_after();
-          for (int t = w.t0; t < w.t1; ++t, ++kv) {
-            const uint32_t buf = kv & 1;
-            if (!wd.wait(&bars[L::bKFull + kv % NK], (kv / NK) & 1)) { stop = true; break; }
-            if (kv >= 2 && !wd.wait(&bars[L::bSEmpty + buf], ((kv >> 1) - 1) & 1)) { stop = true; break; }
-            tc_fence_after();
-            const uint32_t k_addr = smem_u32(sm + L::kK + (kv % NK) * kTB);
+          const int nt = w.t1 - w.t0;
+          for (int j = 0; j < nt && !stop; j += kGroups) {
+            const int batch = min(nt - j, kGroups);
+            for (int half = 0; half < halves && !stop; ++half) {
+              const int cols = min(rows - half * 128, 128), N = max((cols + 15) & ~15, 16);
+              const uint32_t idesc = FP16 ? idesc_f16_f32(128, N, 0, 0) : idesc_bf16_f32(128, N, 0, 0);
+              for (int i = 0; i < batch; ++i) {
+                const uint32_t x = kv + i, y = x % kGroups;
+                if (half == 0 && !wd.wait(&bars[L::bKFull + x % NK], (x / NK) & 1)) { stop = true; break; }
+                if (((ever >> y) & 1u) && !wd.wait(&bars[L::bSEmpty + y], ((odd >> y) & 1u) ^ 1u)) { stop = true; break; }
+                ever |= 1u << y;
+                odd ^= 1u << y;
+                tc_fence_after();
+                const uint32_t k_addr = smem_u32(sm + L::kK + (x % NK) * kTB);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_ss(tmem + buf * 256, sw128_desc(k_addr + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024),
-                     sw128_desc(q_addr + (kk >> 2) * (kRows * 128) + (kk & 3) * 32, 16, 1024), idesc, kk > 0);
-            mma_commit(&bars[L::bSFull + buf]);
-            mma_commit(&bars[L::bKEmpty + kv % NK]);
+                for (int kk = 0; kk < D / 16; ++kk)
+                  mma_ss(tmem + y * 128, sw128_desc(k_addr + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024),
+                         sw128_desc(q_addr + half * 16384 + (kk >> 2) * (kRows * 128) + (kk & 3) * 32, 16, 1024), idesc,
+                         kk > 0);
+                mma_commit(&bars[L::bSFull + y]);
+                if (half == halves - 1) mma_commit(&bars[L::bKEmpty + x % NK]);
+              }
+            }
+            kv += batch;
           }
         }
       }
@@ -152,26 +168,26 @@ __global__ void __launch_bounds__(384, 1) k_weigh(const __grid_constant__ CUtens
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ sums
-    const uint32_t y = (warp - 4) >> 2;  // the tiles with kv mod 2 == y
+    const uint32_t y = (warp - 4) >> 2;  // the tiles with kv mod 4 == y
     const int r = (warp & 3) * 32 + lane, th = threadIdx.x - 128;
-    const uint32_t t_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + y * 256;
+    const uint32_t t_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + y * 128;
     auto wwait = [&](uint64_t *bar, uint32_t parity) {
       return __all_sync(0xffffffffu, wd.wait(bar, parity)) != 0;
     };
     Walk<kAllRows> w(p.cache, p.tok, run);
-    uint32_t kv = 0;
+    uint32_t kv = 0, used = 0;
     bool stop = false;
     while (w.next(p.cache, p.tok)) {
       const int64_t base = (static_cast<int64_t>(w.b) * p.cache.H_kv + w.hk) * p.cache.capacity;
       for (int pass = 0; pass < passes(w); ++pass) {
         const int row0 = pass * kRows, rows = min(w.s.n * G - row0, kRows);
-        // the rows of this pass -> shared memory, once both halves are done with the last pass (after a timeout too:
+        // the rows of this pass -> shared memory, once every group is done with the last pass (after a timeout too:
         // the barriers pair up in every path)
-        named_bar_sync(1, 256);
+        named_bar_sync(1, kSumThreads);
         constexpr int kPieces = D / 8;
         const int padded = max((rows + 15) & ~15, 16);
 #pragma unroll 4
-        for (int i = th; i < padded * kPieces; i += 256) {
+        for (int i = th; i < padded * kPieces; i += kSumThreads) {
           const int rr = i / kPieces, c = i % kPieces, grow = row0 + rr;
           int4 v = make_int4(0, 0, 0, 0);
           if (rr < rows)
@@ -179,71 +195,83 @@ __global__ void __launch_bounds__(384, 1) k_weigh(const __grid_constant__ CUtens
                                                 (w.hk * G + grow % G) * p.qs[2] + c * 8);
           *reinterpret_cast<int4 *>(sm + L::kQ + (c >> 3) * (kRows * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v;
         }
-        {
+        if (th < kRows) {
           const int grow = row0 + th, tok = grow / G, h = w.hk * G + grow % G;
           float z = -INFINITY;
-          uint64_t word = 0;
           if (th < rows) {
             const float x = p.lse[(static_cast<int64_t>(w.b) * p.tok.H + h) * p.tok.T + tok];
             z = x == -INFINITY ? -INFINITY : -x * kLog2e;
-            word = tree_word(p.tok, w.b, tok, w.s.n);
           }
           nlse[th] = z;
-          words[th] = static_cast<uint32_t>(word);
-          words[kRows + th] = static_cast<uint32_t>(word >> 32);
+        } else if (th - kRows < kMaxTok) {
+          const int tok = th - kRows;
+          words[tok] = tok < w.s.n ? tree_word(p.tok, w.b, tok, w.s.n) : 0ull;
         }
         fence_proxy_async_smem();
-        named_bar_sync(2, 256);
+        named_bar_sync(2, kSumThreads);
         if (th == 0) mbar_arrive(&bars[L::bQFull]);
+        const int halves = rows > 128 ? 2 : 1;
         for (int t = w.t0; t < w.t1; ++t, ++kv) {
-          if ((kv & 1) != y || stop) continue;
+          if (kv % kGroups != y || stop) continue;
           const int j = t * kTile + r, d = j - w.s.len;  // this thread's slot; a new token where d >= 0
-          const bool live = d < w.s.n;
+          const bool live = d < w.s.n, edge = t * kTile + kTile > w.s.len;
           float before = 0.f;
           if (live) before = pass == 0 ? p.score_in[base + j] : p.score_out[base + j];
-          if (!wwait(&bars[L::bSFull + y], (kv >> 1) & 1)) { stop = true; continue; }
-          tc_fence_after();
-          const bool edge = t * kTile + kTile > w.s.len;
           const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
-          float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
-          uint32_t sv[2][16];
-          tmem_ld16(t_s, sv[0]);
-          tmem_wait_ld();
-          for (int c0 = 0; c0 < rows; c0 += 32) {
+          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          for (int half = 0; half < halves; ++half) {
+            const float *zs = nlse + half * 128;
+            const int cols = min(rows - half * 128, 128);
+            if (!wwait(&bars[L::bSFull + y], used & 1)) { stop = true; break; }
+            ++used;
+            tc_fence_after();
+            int c = 0;
+            uint32_t s[32];
+            if (!edge) {
+#pragma unroll 1
+              for (; c + 32 <= cols; c += 32) {
+                tmem_ld32(t_s + c, s);
+                tmem_wait_ld();
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int c = c0 + 16 * half;
-              if (c < rows) {
-                if (c + 16 < rows) tmem_ld16(t_s + c + 16, sv[half ^ 1]);
-                const uint32_t *s = sv[half];
-                if (!edge && c + 16 <= rows) {
-#pragma unroll
-                  for (int q = 0; q < 4; ++q) {
-                    const float4 z = *reinterpret_cast<const float4 *>(nlse + c + 4 * q);
-                    const float2 e0 = __ffma2_rn(make_float2(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])), sc2,
-                                                 make_float2(z.x, z.y));
-                    const float2 e1 = __ffma2_rn(make_float2(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])),
-                                                 sc2, make_float2(z.z, z.w));
-                    acc0 = __fadd2_rn(acc0, make_float2(fast_exp2(e0.x), fast_exp2(e0.y)));
-                    acc1 = __fadd2_rn(acc1, make_float2(fast_exp2(e1.x), fast_exp2(e1.y)));
-                  }
-                } else {
-                  // columns past the rows, and rows that do not see this new token, add nothing whatever they hold
-#pragma unroll
-                  for (int q = 0; q < 16; ++q) {
-                    const uint32_t wd32 = words[(d >= 32 ? kRows : 0) + c + q];
-                    const bool on = c + q < rows && nlse[c + q] != -INFINITY && (d < 0 || ((wd32 >> (d & 31)) & 1u));
-                    const float e = fast_exp2(fmaf(__uint_as_float(s[q]), p.scale_log2, nlse[c + q]));
-                    acc0.x += on ? e : 0.f;
-                  }
+                for (int q = 0; q < 8; ++q) {
+                  const float4 z = *reinterpret_cast<const float4 *>(zs + c + 4 * q);
+                  const float2 e0 = __ffma2_rn(make_float2(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])), sc2,
+                                               make_float2(z.x, z.y));
+                  const float2 e1 = __ffma2_rn(make_float2(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])),
+                                               sc2, make_float2(z.z, z.w));
+                  acc[2 * (q & 1)] = __fadd2_rn(acc[2 * (q & 1)], make_float2(fast_exp2(e0.x), fast_exp2(e0.y)));
+                  acc[2 * (q & 1) + 1] = __fadd2_rn(acc[2 * (q & 1) + 1], make_float2(fast_exp2(e1.x), fast_exp2(e1.y)));
                 }
-                if (c + 16 < rows) tmem_wait_ld();
               }
             }
+            // the last columns, and tiles with new tokens: columns past the rows, and rows that do not see this
+            // thread's token, add nothing whatever they hold
+#pragma unroll 1
+            for (; c < cols; c += 32) {
+              tmem_ld32(t_s + c, s);
+              tmem_wait_ld();
+              uint32_t on = cols - c >= 32 ? 0xffffffffu : (1u << (cols - c)) - 1u;
+              if (edge && d >= 0) {
+                // the columns of the tokens that see new token d
+                const int first = row0 + half * 128 + c;
+                uint32_t sees = 0;
+#pragma unroll 4
+                for (int tok = first / G; tok * G < first + 32 && tok < w.s.n; ++tok)
+                  if ((words[tok] >> (d & 63)) & 1ull) sees |= range_bits(tok * G - first, tok * G - first + G - 1, 0);
+                on &= sees;
+              }
+#pragma unroll
+              for (int q = 0; q < 32; ++q) {
+                const float e = fast_exp2(fmaf(__uint_as_float(s[q]), p.scale_log2, zs[c + q]));
+                acc[q & 3].x += ((on >> q) & 1u) ? e : 0.f;
+              }
+            }
+            tc_fence_before();
+            mbar_arrive(&bars[L::bSEmpty + y]);
           }
-          tc_fence_before();
-          mbar_arrive(&bars[L::bSEmpty + y]);
-          if (live) p.score_out[base + j] = before + ((acc0.x + acc1.x) + (acc0.y + acc1.y));
+          if (live && !stop)
+            p.score_out[base + j] =
+                before + (((acc[0].x + acc[1].x) + (acc[2].x + acc[3].x)) + ((acc[0].y + acc[1].y) + (acc[2].y + acc[3].y)));
         }
       }
     }
@@ -264,7 +292,7 @@ cudaError_t launch(const WeighParams &p, const CUtensorMap &tk, int ctas, cudaSt
   const cudaError_t e = cudaFuncSetAttribute(k_weigh<FP16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
   if (e != cudaSuccess) return e;
   count_launch();
-  k_weigh<FP16, D><<<ctas, 384, L::kAlloc, s>>>(tk, p);
+  k_weigh<FP16, D><<<ctas, 128 + kSumThreads, L::kAlloc, s>>>(tk, p);
   return cudaGetLastError();
 }
 
