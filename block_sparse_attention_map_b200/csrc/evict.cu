@@ -8,15 +8,25 @@
 // i-th into the i-th.  Sources lie at or past the budget and destinations below
 // it, so the moves need no order among themselves and touch only what changes.
 //
-// k_evict_select: one CTA per head; four 8-bit histogram passes find the key at
-// the budget, then one ordered pass numbers ties, holes and movers.
-// k_evict_move: a group of D/8 lanes moves one slot's K and V, 16 bytes a lane.
+// k_evict_select: a cluster of up to 8 CTAs per head, each with an equal share of
+// the head's slots in slot order and their keys in shared memory.  Four 8-bit
+// histogram passes (the CTAs' histograms summed over distributed shared memory)
+// find the key at the budget; two ordered counts over warps and CTAs then number
+// ties, holes and movers.  Bound: the latency of the passes, about 1 us each; one
+// CTA a head took 337 us for 65536 slots and 49 us for 4097.
+// k_evict_move: a group of D/8 lanes moves one slot's K and V, 16 bytes a lane,
+// over all SMs.  Bound: HBM.
+#include <cooperative_groups.h>
+
 #include "serving.cuh"
 
 namespace bsa {
 namespace {
 
-constexpr int kSelThreads = 1024;
+namespace cg = cooperative_groups;
+
+constexpr int kMaxSelCtas = 8;      // a portable cluster
+constexpr int kMaxKeys = 48 * 1024;  // of a CTA's slots in shared memory (more are read again for each pass)
 
 __device__ __forceinline__ uint32_t score_key(float s) {
   if (s != s) return 0u;
@@ -28,54 +38,191 @@ struct HeadKeys {
   const float *score;
   const int32_t *pos;
   int sinks, recent_from;
-  __device__ __forceinline__ uint32_t operator()(int i) const {
-    const int p = pos[i];
-    return p < sinks || p >= recent_from ? 0xffffffffu : score_key(score[i]);
+  __device__ __forceinline__ uint32_t of(int p, float sc) const {
+    return p < sinks || p >= recent_from ? 0xffffffffu : score_key(sc);
   }
+  __device__ __forceinline__ uint32_t operator()(int i) const { return of(pos[i], score[i]); }
 };
 
-__global__ void __launch_bounds__(kSelThreads) k_evict_select(const EvictArgs a) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t sel[2];       // chosen digit, what is still wanted within it
-  __shared__ int warp_tot[3][32];
-  const int head = blockIdx.x, b = head / a.cache.H_kv;
+// Exclusive prefix over the CTA's warps of two counts a warp, by every thread of
+// the CTA; the CTA's totals are left in warp_n[kSelWarps].
+template <int kSelWarps>
+__device__ __forceinline__ int2 count_warps(int2 (&warp_n)[kSelWarps + 1], int2 n) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) warp_n[warp] = n;
+  __syncthreads();
+  if (warp == 0) {
+    const int2 v = lane < kSelWarps ? warp_n[lane] : make_int2(0, 0);
+    int2 incl = v;
+#pragma unroll
+    for (int d = 1; d < kSelWarps; d <<= 1) {
+      const int ox = __shfl_up_sync(0xffffffffu, incl.x, d), oy = __shfl_up_sync(0xffffffffu, incl.y, d);
+      if (lane >= d) {
+        incl.x += ox;
+        incl.y += oy;
+      }
+    }
+    if (lane < kSelWarps) warp_n[lane] = make_int2(incl.x - v.x, incl.y - v.y);
+    if (lane == kSelWarps - 1) warp_n[kSelWarps] = incl;
+  }
+  __syncthreads();
+  return warp_n[warp];
+}
+
+// K > 0: a thread's keys in K registers; K = 0: in shared memory where key_cap
+// holds them, else read again by each pass.
+template <int kSelThreads, int K>
+__global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) k_evict_select(const EvictArgs a, int key_cap) {
+  constexpr int kSelWarps = kSelThreads / 32;
+  extern __shared__ uint32_t keys[];  // [key_cap]: this CTA's, where they fit
+  __shared__ __align__(16) uint32_t hist[2][256];   // one a pass by turns, so that a pass needs one cluster barrier
+  __shared__ uint32_t sel[3];         // chosen digit, what is still wanted within it, the keys of it in lower CTAs
+  __shared__ int2 counts[2][kSelWarps + 1];
+  cg::cluster_group cluster = cg::this_cluster();
+  const unsigned ctas = cluster.num_blocks(), rank = cluster.block_rank();
+  const int head = blockIdx.x / ctas, b = head / a.cache.H_kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t base = static_cast<int64_t>(head) * a.cache.capacity;
-  const int n = clamped_length(a.cache, b, tid == 0);
+  const int n = clamped_length(a.cache, b, tid == 0 && rank == 0);
   const float *score = a.score_in + base;
   const int32_t *pos = a.pos_in + base;
   float *score_out = a.score_out + base;
   int32_t *pos_out = a.pos_out + base;
-  if (n <= a.budget) {
-    if (tid == 0) a.count[head] = 0;
+  pdl_trigger();
+  if (n <= a.budget) {  // the whole cluster
+    if (tid == 0 && rank == 0) a.count[head] = 0;
     if (score_out != score)
-      for (int i = tid; i < n; i += kSelThreads) score_out[i] = score[i];
+      for (int i = rank * kSelThreads + tid; i < n; i += ctas * kSelThreads) score_out[i] = score[i];
     if (pos_out != pos)
-      for (int i = tid; i < n; i += kSelThreads) pos_out[i] = pos[i];
+      for (int i = rank * kSelThreads + tid; i < n; i += ctas * kSelThreads) pos_out[i] = pos[i];
     return;
   }
   // next_pos - recent below the int32 range: everything is recent
   const int64_t rf = static_cast<int64_t>(a.next_pos[b]) - a.recent;
-  const HeadKeys key{score, pos, a.sinks, static_cast<int>(rf < INT_MIN ? INT_MIN : rf)};
+  const HeadKeys key_of{score, pos, a.sinks, static_cast<int>(rf < INT_MIN ? INT_MIN : rf)};
+
+  // this warp's slots [w0, w1), in slot order over the warps of the cluster's CTAs
+  const int chunks = (n + 31) / 32, per_warp = (chunks + ctas * kSelWarps - 1) / (ctas * kSelWarps) * 32;
+  const int s0 = static_cast<int>(rank) * kSelWarps * per_warp;  // the CTA's first
+  const int w0 = min(s0 + warp * per_warp, n), w1 = min(w0 + per_warp, n);
+  const bool kept_here = kSelWarps * per_warp <= key_cap;
+  uint32_t regs[K > 0 ? K : 1];
+  // f(k, slot) for the warp's slots in order, 32 at a time, by all lanes (the last slots may lie at or past w1)
+  auto each = [&](auto f) {
+    if constexpr (K > 0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (w0 + 32 * k < w1) f(k, w0 + 32 * k + lane);
+    } else {
+#pragma unroll 4
+      for (int i0 = w0; i0 < w1; i0 += 32) f(0, i0 + lane);
+    }
+  };
+  auto key = [&](int k, int i) {
+    if constexpr (K > 0) return regs[k];
+    else return i >= w1 ? 0u : kept_here ? keys[i - s0] : key_of(i);
+  };
+  for (int i = tid; i < 256; i += kSelThreads) hist[0][i] = 0;
+  if constexpr (K > 0) {
+    int ps[K];
+    float sc[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {  // all loads in flight
+      const int i = min(w0 + 32 * k + lane, n - 1);
+      ps[k] = pos[i];
+      sc[k] = score[i];
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) regs[k] = w0 + 32 * k + lane < w1 ? key_of.of(ps[k], sc[k]) : 0u;
+  } else if (kept_here) {
+    constexpr int U = 8;  // loads of U slots in flight
+    for (int i0 = w0 + lane; i0 < w1; i0 += 32 * U) {
+      int ps[U];
+      float sc[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = min(i0 + 32 * u, n - 1);
+        ps[u] = pos[i];
+        sc[u] = score[i];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + 32 * u < w1) keys[i0 + 32 * u - s0] = key_of.of(ps[u], sc[u]);
+    }
+  }
+  __syncthreads();
 
   // the key at the budget, digit by digit from the top
   uint32_t prefix = 0, want = static_cast<uint32_t>(a.budget);
 #pragma unroll 1
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
-    for (int i = tid; i < n; i += kSelThreads) {
-      const uint32_t x = key(i);
-      if ((x & mask) == prefix) atomicAdd(&hist[(x >> shift) & 255u], 1u);
-    }
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t left = want;
-      int d = 255;
-      for (; d > 0 && hist[d] < left; --d) left -= hist[d];
-      sel[0] = static_cast<uint32_t>(d);
-      sel[1] = left;
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    uint32_t *mine = hist[pass & 1];
+    const uint32_t mask = pass == 0 ? 0u : ~0u << (shift + 8);
+    each([&](int k, int i) {
+      const uint32_t x = key(k, i);
+      if (i < w1 && (x & mask) == prefix) atomicAdd(&mine[(x >> shift) & 255u], 1u);
+    });
+    if (ctas > 1) cluster.sync();
+    else __syncthreads();
+    if (warp == 0) {
+      // lane l: the digits 255 - 8 l down to 248 - 8 l
+      uint32_t v[8], sum = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = 0;
+      uint32_t low[8];  // of the CTAs before this one
+#pragma unroll
+      for (int k = 0; k < 8; ++k) low[k] = 0;
+      if (ctas == 1) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = mine[255 - 8 * lane - k];
+      } else {
+#pragma unroll 1
+        for (unsigned c0 = 0; c0 < ctas; c0 += 4) {
+          uint4 x[4], y[4];  // four CTAs' loads in flight (a cluster is 1, 4 or 8)
+#pragma unroll
+          for (unsigned c = 0; c < 4; ++c) {
+            const uint4 *theirs = reinterpret_cast<const uint4 *>(cluster.map_shared_rank(mine, c0 + c) + 248 - 8 * lane);
+            x[c] = theirs[0];
+            y[c] = theirs[1];
+          }
+#pragma unroll
+          for (unsigned c = 0; c < 4; ++c) {
+            const uint32_t t8[8] = {y[c].w, y[c].z, y[c].y, y[c].x, x[c].w, x[c].z, x[c].y, x[c].x};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              v[k] += t8[k];
+              low[k] += c0 + c < rank ? t8[k] : 0u;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum += v[k];
+      uint32_t incl = sum;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      const uint32_t excl = incl - sum;
+      if (excl < want && want <= incl) {  // one lane
+        uint32_t left = want - excl;
+        bool found = false;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (!found && v[k] >= left) {
+            found = true;
+            sel[0] = static_cast<uint32_t>(255 - 8 * lane - k);
+            sel[1] = left;
+            sel[2] = low[k];
+          }
+          if (!found) left -= v[k];
+        }
+      }
+    } else {
+      // the next pass's histogram: its last readers passed the barrier above
+      for (int i = tid - 32; i < 256; i += kSelThreads - 32) hist[(pass + 1) & 1][i] = 0;
     }
     __syncthreads();
     prefix |= sel[0] << shift;
@@ -83,90 +230,128 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const EvictArgs a)
     __syncthreads();
   }
 
-  // in slot order: keep keys above `prefix` and the first `want` equal to it
-  int ties = 0, holes = 0, movers = 0;  // so far, over the chunks done
+  // In slot order: keep keys above `prefix` and the first `want` equal to it.  The
+  // warp's equal keys, those of them below the budget, and of the other keys the
+  // holes and movers; which equal keys stay follows from how many came before.
+  const uint32_t below = (1u << lane) - 1u;
+  int ties = 0, low_ties = 0, holes = 0, movers = 0;
+  each([&](int k, int i) {
+    const bool in = i < w1;
+    const uint32_t x = key(k, i);
+    const uint32_t tb = __ballot_sync(0xffffffffu, in && x == prefix), lb = __ballot_sync(0xffffffffu, i < a.budget);
+    ties += __popc(tb);
+    low_ties += __popc(tb & lb);
+    holes += __popc(__ballot_sync(0xffffffffu, in && x < prefix) & lb);
+    movers += __popc(__ballot_sync(0xffffffffu, in && x > prefix) & ~lb);
+  });
+  // equal keys of lower CTAs (from the last pass's histograms) and lower warps
+  const int ties_before = static_cast<int>(sel[2]) + count_warps<kSelWarps>(counts[0], make_int2(ties, 0)).x;
+  const int tie_keep = min(max(static_cast<int>(want) - ties_before, 0), ties), low_keep = min(tie_keep, low_ties);
+  holes += low_ties - low_keep;
+  movers += tie_keep - low_keep;
+  const int2 in_cta = count_warps<kSelWarps>(counts[1], make_int2(holes, movers));
+  int hole_at = in_cta.x, mover_at = in_cta.y, moved = counts[1][kSelWarps].y;
+  if (ctas > 1) {
+    cluster.sync();
+    moved = 0;
+    int2 t[kMaxSelCtas];
+#pragma unroll
+    for (unsigned c = 0; c < kMaxSelCtas; ++c)
+      t[c] = c < ctas ? cluster.map_shared_rank(&counts[1][kSelWarps], c)[0] : make_int2(0, 0);
+#pragma unroll
+    for (unsigned c = 0; c < kMaxSelCtas; ++c) {
+      hole_at += c < rank ? t[c].x : 0;
+      mover_at += c < rank ? t[c].y : 0;
+      moved += t[c].y;
+    }
+  }
   int32_t *to = a.to + static_cast<int64_t>(head) * a.list_cap;
   int32_t *from = a.from + static_cast<int64_t>(head) * a.list_cap;
   int32_t *mpos = a.mpos + static_cast<int64_t>(head) * a.list_cap;
   float *mscore = a.mscore + static_cast<int64_t>(head) * a.list_cap;
-  const uint32_t below = (1u << lane) - 1u;
-  for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-    const int i = i0 + tid;
-    const bool in = i < n;
-    const uint32_t x = in ? key(i) : 0u;
-    const bool tie = in && x == prefix;
-    const uint32_t tb = __ballot_sync(0xffffffffu, tie);
-    if (lane == 0) warp_tot[0][warp] = __popc(tb);
-    __syncthreads();
-    int before = ties + __popc(tb & below), all = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) before += warp_tot[0][w];
-      all += warp_tot[0][w];
-    }
-    ties += all;
-    const bool keep = in && (x > prefix || (tie && before < static_cast<int>(want)));
-    const bool hole = in && !keep && i < a.budget, mover = keep && i >= a.budget;
+  // Kept slots below the budget stay where they are: nothing to do for them where
+  // the outputs are the inputs.
+  const bool copies = score_out != score || pos_out != pos;
+  int seen = ties_before;
+  each([&](int kk, int i) {
+    const bool in = i < w1;
+    const uint32_t x = key(kk, i);
+    const uint32_t tb = __ballot_sync(0xffffffffu, in && x == prefix);
+    const bool k = in && (x > prefix || (x == prefix && seen + __popc(tb & below) < static_cast<int>(want)));
+    seen += __popc(tb);
+    const bool hole = in && !k && i < a.budget, mover = k && i >= a.budget;
     const uint32_t hb = __ballot_sync(0xffffffffu, hole), mb = __ballot_sync(0xffffffffu, mover);
-    if (lane == 0) {
-      warp_tot[1][warp] = __popc(hb);
-      warp_tot[2][warp] = __popc(mb);
-    }
-    __syncthreads();
-    int hi = holes + __popc(hb & below), mi = movers + __popc(mb & below), ha = 0, ma = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) {
-        hi += warp_tot[1][w];
-        mi += warp_tot[2][w];
-      }
-      ha += warp_tot[1][w];
-      ma += warp_tot[2][w];
-    }
-    holes += ha;
-    movers += ma;
-    if (hole) to[hi] = i;
-    if (mover) {
-      from[mi] = i;
-      mpos[mi] = pos[i];
-      mscore[mi] = score[i];
-    }
-    if (in) {
-      // movers were read above by this thread; holes are filled by the move
-      if (i >= a.budget) {
-        score_out[i] = 0.f;
-        pos_out[i] = -1;
-      } else if (keep) {
-        score_out[i] = score[i];
-        pos_out[i] = pos[i];
+    // (never past the lists, whatever another stream does to the inputs meanwhile)
+    const int ha = hole_at + __popc(hb & below), ma = mover_at + __popc(mb & below);
+    if (hole && ha < a.list_cap) to[ha] = i;
+    const bool copy = k && copies && i < a.budget;  // (holes are filled by the move)
+    if (mover || copy) {
+      const float sc = score[i];
+      const int ps = pos[i];
+      if (copy) {
+        score_out[i] = sc;
+        pos_out[i] = ps;
+      } else if (ma < a.list_cap) {
+        from[ma] = i;
+        mpos[ma] = ps;
+        mscore[ma] = sc;
       }
     }
-  }
-  if (tid == 0) a.count[head] = movers;
+    if (in && i >= a.budget) {
+      score_out[i] = 0.f;
+      pos_out[i] = -1;
+    }
+    hole_at += __popc(hb);
+    mover_at += __popc(mb);
+  });
+  if (tid == 0 && rank == 0) a.count[head] = min(moved, a.list_cap);
+  if (ctas > 1) cluster.sync();  // no CTA leaves while another may read its shared memory
 }
 
 template <int D>
 __global__ void __launch_bounds__(256) k_evict_move(const EvictArgs a, int per_head) {
   constexpr int L = D / 8;  // lanes a row
+  constexpr int kMoves = 256 / L, U = 2;  // moves of a block at a time, each group with U of them in flight
   const int head = blockIdx.x / per_head, part = blockIdx.x % per_head;
   const int b = head / a.cache.H_kv, hk = head % a.cache.H_kv;
   const int sub = threadIdx.x % L, grp = threadIdx.x / L;
-  constexpr int kGroups = 256 / L;
   pdl_wait();
+  // the block's moves of a step lie next to each other (rows of one DRAM page: 74 us with the groups' moves apart)
   const int m = a.count[head];
   const int64_t lb = static_cast<int64_t>(head) * a.list_cap, base = static_cast<int64_t>(head) * a.cache.capacity;
-  for (int i = part * kGroups + grp; i < m; i += per_head * kGroups) {
-    const int to = a.to[lb + i], from = a.from[lb + i];
-    const int pt = page_of(a.cache, b, to), pf = page_of(a.cache, b, from);
-    if (pt >= 0 && pf >= 0) {
-      const int4 kv = *reinterpret_cast<const int4 *>(a.cache.k + slot_offset(a.cache.ks, a.cache, pf, from, hk) + sub * 8);
-      const int4 vv = *reinterpret_cast<const int4 *>(a.cache.v + slot_offset(a.cache.vs, a.cache, pf, from, hk) + sub * 8);
-      *reinterpret_cast<int4 *>(a.cache.k + slot_offset(a.cache.ks, a.cache, pt, to, hk) + sub * 8) = kv;
-      *reinterpret_cast<int4 *>(a.cache.v + slot_offset(a.cache.vs, a.cache, pt, to, hk) + sub * 8) = vv;
-    } else if (sub == 0) {
-      record_status(a.cache.status, BSA_ERR_BAD_CACHE);
+  for (int i0 = part * U * kMoves + grp; i0 < m; i0 += per_head * U * kMoves) {
+    int to[U], from[U], pt[U], pf[U];
+    int4 kv[U], vv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kMoves;
+      to[u] = i < m ? a.to[lb + i] : -1;
+      from[u] = i < m ? a.from[lb + i] : -1;
     }
-    if (sub == 0) {
-      a.score_out[base + to] = a.mscore[lb + i];
-      a.pos_out[base + to] = a.mpos[lb + i];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      pt[u] = to[u] >= 0 ? page_of(a.cache, b, to[u]) : -1;
+      pf[u] = to[u] >= 0 ? page_of(a.cache, b, from[u]) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (pt[u] < 0 || pf[u] < 0) continue;
+      kv[u] = *reinterpret_cast<const int4 *>(a.cache.k + slot_offset(a.cache.ks, a.cache, pf[u], from[u], hk) + sub * 8);
+      vv[u] = *reinterpret_cast<const int4 *>(a.cache.v + slot_offset(a.cache.vs, a.cache, pf[u], from[u], hk) + sub * 8);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (to[u] < 0) continue;
+      if (pt[u] >= 0 && pf[u] >= 0) {
+        *reinterpret_cast<int4 *>(a.cache.k + slot_offset(a.cache.ks, a.cache, pt[u], to[u], hk) + sub * 8) = kv[u];
+        *reinterpret_cast<int4 *>(a.cache.v + slot_offset(a.cache.vs, a.cache, pt[u], to[u], hk) + sub * 8) = vv[u];
+      } else if (sub == 0) {
+        record_status(a.cache.status, BSA_ERR_BAD_CACHE);
+      }
+      if (sub == 0) {
+        a.score_out[base + to[u]] = a.mscore[lb + i0 + u * kMoves];
+        a.pos_out[base + to[u]] = a.mpos[lb + i0 + u * kMoves];
+      }
     }
   }
   if (part == 0 && hk == 0 && threadIdx.x == 0) {
@@ -176,13 +361,49 @@ __global__ void __launch_bounds__(256) k_evict_move(const EvictArgs a, int per_h
   }
 }
 
+template <int THREADS, int K>
+cudaError_t select(const EvictArgs &a, int heads, int ctas, cudaStream_t s) {
+  constexpr int kWarps = THREADS / 32;
+  // a CTA's slots, at most
+  const int share = ((a.cache.capacity + 31) / 32 + ctas * kWarps - 1) / (ctas * kWarps) * THREADS;
+  const int key_cap = K == 0 && share <= kMaxKeys ? share : 0;
+  cudaError_t e = cudaSuccess;
+  if (K == 0 &&
+      (e = cudaFuncSetAttribute(k_evict_select<THREADS, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4)) !=
+          cudaSuccess)
+    return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(heads) * ctas);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = static_cast<size_t>(key_cap) * 4;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  count_launch(2);
+  return cudaLaunchKernelEx(&cfg, k_evict_select<THREADS, K>, a, key_cap);
+}
+
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s) {
   const int heads = a.cache.B * a.cache.H_kv;
-  count_launch(2);
-  k_evict_select<<<heads, kSelThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  // A head's slots are 8 a thread of one CTA up to 8192 (few slots in a large CTA
+  // are slots for no one: 512 heads of 1025 slots 39 us with 1024 threads), else of
+  // a cluster of CTAs of 512 threads, so that an SM holds two (16 clusters of 8 x
+  // 1024 did not fit the GPU at once: 85 us against 37 for the selection of 65536).
+  const int cap = a.cache.capacity;
+  cudaError_t e;
+  if (cap <= 2048) e = select<256, 8>(a, heads, 1, s);
+  else if (cap <= 4096) e = select<512, 8>(a, heads, 1, s);
+  else if (cap <= 8192) e = select<1024, 8>(a, heads, 1, s);
+  else if (cap <= 16384) e = select<512, 8>(a, heads, 4, s);
+  else if (cap <= 32768) e = select<512, 8>(a, heads, 8, s);
+  else e = select<512, 0>(a, heads, 8, s);  // (16 keys a thread spill: 43 us against 37 for 65536)
   if (e != cudaSuccess) return e;
   const int per_head = std::max(1, std::min((148 * 8 + heads - 1) / heads, (a.list_cap + 15) / 16));
   return a.cache.D == 64

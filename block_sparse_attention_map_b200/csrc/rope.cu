@@ -4,11 +4,15 @@
 //   angle = pos[axis[p], b, t] * inv_freq[p]
 //   y0 = x0 cos - x1 sin,  y1 = x0 sin + x1 cos     (inverse: sin -> -sin)
 //
-// A thread owns one 16-byte chunk of a token (4 interleaved pairs, or 8 pairs
-// as one chunk of each half), takes the chunk's sines and cosines once, and
-// walks the token's heads with them.  Consecutive threads are consecutive
-// chunks, then heads: a warp moves 512 contiguous bytes.  Bound: HBM; the only
-// reads besides the tensors are the positions and the two small tables.
+// A block takes a few tokens: its threads compute the tokens' sines and cosines
+// once, into shared memory (a thread for each pair and token), then each thread
+// holds those of 8 pairs (a 16-byte chunk of each half, or two chunks of 4
+// interleaved pairs D/2 elements apart) and walks a share of the token's heads with them.  Consecutive
+// threads are consecutive chunks, then heads: a warp moves 512 contiguous bytes.
+// Bound: HBM; the only reads besides the tensors are the positions and the two
+// small tables.  (A thread that computed its own chunk's sines for each share of
+// the heads spent more time on them than on the rows where heads are few: 8192
+// tokens x 20 heads 30 us, now 17.)
 //
 // The angle is reduced before any rounding to 32 bits: the frequency in turns
 // is a 64-bit fraction of a turn, so its product with the integer position
@@ -20,27 +24,36 @@
 namespace bsa {
 namespace {
 
-// The angle's sine and cosine; false for a pair that is copied.
-__device__ __forceinline__ bool pair_turn(const RopeArgs &a, int p, int b, int t, float &c, float &s) {
-  c = 1.f;
-  s = 0.f;
-  if (!a.rotate || p >= a.n_pairs) return false;
+// A pair's frequency as a 64-bit fraction of a turn, and its axis (-1: the pair is
+// copied).
+struct Pair {
+  uint64_t frac;
+  int axis;
+};
+
+__device__ __forceinline__ Pair pair_of(const RopeArgs &a, int p) {
+  if (p >= a.n_pairs) return Pair{0, -1};
   const int ax = a.axis[p];
-  if (static_cast<unsigned>(ax) >= static_cast<unsigned>(a.n_axes)) return false;
-  const int64_t pos = a.pos[ax * a.pos_s[0] + b * a.pos_s[1] + t];
+  if (static_cast<unsigned>(ax) >= static_cast<unsigned>(a.n_axes)) return Pair{0, -1};
   double f = a.inv_freq[p] * 0.15915494309189535;  // 1 / (2 pi)
   f -= floor(f);
-  const uint64_t frac = f >= 0.0 && f < 1.0 ? static_cast<uint64_t>(f * 18446744073709551616.0) : 0ull;
-  const uint64_t turn = static_cast<uint64_t>(pos) * frac;
+  return Pair{f >= 0.0 && f < 1.0 ? static_cast<uint64_t>(f * 18446744073709551616.0) : 0ull, ax};
+}
+
+__device__ __forceinline__ void turn_of(const RopeArgs &a, const Pair &p, int b, int t, float &c, float &s) {
+  c = 1.f;
+  s = 0.f;
+  if (p.axis < 0) return;
+  const int64_t pos = a.pos[p.axis * a.pos_s[0] + b * a.pos_s[1] + t];
+  const uint64_t turn = static_cast<uint64_t>(pos) * p.frac;
   const int32_t top = static_cast<int32_t>((turn + 0x80000000ull) >> 32);
   sincospif(static_cast<float>(top) * 4.656612873077393e-10f /* 2^-31 */, &s, &c);
   if (a.inverse) s = -s;
-  return true;
 }
 
 // Eight rotated elements as four pairs side by side.
 template <bool FP16>
-__device__ __forceinline__ int4 turn_interleaved(int4 v, const float (&c)[4], const float (&s)[4], uint32_t rot) {
+__device__ __forceinline__ int4 turn_interleaved(int4 v, const float *c, const float *s, uint32_t rot) {
   uint32_t w[4] = {static_cast<uint32_t>(v.x), static_cast<uint32_t>(v.y), static_cast<uint32_t>(v.z),
                    static_cast<uint32_t>(v.w)};
 #pragma unroll
@@ -73,125 +86,148 @@ __device__ __forceinline__ void turn_halves(int4 &v0, int4 &v1, const float (&c)
   v1 = make_int4(y[0], y[1], y[2], y[3]);
 }
 
-struct HeadPtr {
-  const uint16_t *src;
-  uint16_t *dst;
-  bool turn;
+struct RopeGrid {
+  int n_heads, n_chunks, tokens, lanes;  // a block's step: tokens x lanes (shares of the heads) x chunks
+  int pairs;                             // whose sines are computed (0: k and v as they are)
 };
 
-// Where head i of the list [q heads, k heads, v heads (append)] of a token lies;
-// dst null: nothing to do.
-__device__ __forceinline__ HeadPtr head_ptr(const RopeArgs &a, int i, int b, int t, int64_t k_off, int64_t v_off) {
-  HeadPtr r{nullptr, nullptr, true};
-  const int nq = a.q != nullptr ? a.H : 0;
-  if (i < nq) {
-    r.src = a.q + b * a.qs[0] + t * a.qs[1] + i * a.qs[2];
-    r.dst = a.qo + b * a.qos[0] + t * a.qos[1] + i * a.qos[2];
-    return r;
-  }
-  i -= nq;
-  if (!a.append) {
-    r.src = a.k + b * a.ks[0] + t * a.ks[1] + i * a.ks[2];
-    r.dst = a.ko + b * a.kos[0] + t * a.kos[1] + i * a.kos[2];
-    return r;
-  }
-  if (k_off < 0) return r;  // padding token, or no valid page
-  if (i < a.H_kv) {
-    r.src = a.k + b * a.ks[0] + t * a.ks[1] + i * a.ks[2];
-    r.dst = a.cache.k + k_off + i * a.cache.ks[2];
-  } else {
-    i -= a.H_kv;
-    r.src = a.v + b * a.vs[0] + t * a.vs[1] + i * a.vs[2];
-    r.dst = a.cache.v + v_off + i * a.cache.vs[2];
-    r.turn = false;
-  }
-  return r;
-}
-
 template <bool FP16, bool HALVES>
-__global__ void __launch_bounds__(256) k_rope(const RopeArgs a, int n_heads, int n_chunks, int head_split) {
-  constexpr int P = HALVES ? 8 : 4;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int c = static_cast<int>(unit % n_chunks);
-  const int64_t rest = unit / n_chunks;
-  const int h0 = static_cast<int>(rest % head_split);
-  const int64_t row = rest / head_split;
-  if (row >= static_cast<int64_t>(a.B) * a.T) return;
-  const int b = static_cast<int>(row / a.T), t = static_cast<int>(row % a.T);
+__global__ void __launch_bounds__(256, 4) k_rope(const RopeArgs a, const RopeGrid g) {
+  constexpr int P = 8;  // pairs of a thread: one chunk of each half's, or two chunks of four
+  constexpr int U = 2;  // heads in flight
+  extern __shared__ float trig[];    // two of: cos [tokens][pairs], sin likewise; then which pairs turn
+  const int pairs = g.pairs;
+  uint8_t *turn_sm = reinterpret_cast<uint8_t *>(trig + 4 * g.tokens * pairs);
+  const int rows = a.B * a.T, step = gridDim.x * g.tokens;  // rows < 2^31
 
-  // this thread's elements: one chunk, or one of each half
-  const int pair_chunks = HALVES ? a.n_pairs >> 3 : n_chunks;
-  const bool both = HALVES && c < pair_chunks;
-  const int e0 = HALVES && !both ? (c + pair_chunks) * 8 : c * 8;
-  const int e1 = both ? a.n_pairs + c * 8 : e0;
-  float cs[P], sn[P];
-  uint32_t rot = 0;
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    cs[i] = 1.f;
-    sn[i] = 0.f;
-    if (!HALVES || both) rot |= (pair_turn(a, c * P + i, b, t, cs[i], sn[i]) ? 1u : 0u) << i;
+  // the sines' side: this thread's pair, and every n_sub-th token of a step
+  const int n_sub = pairs > 0 ? 256 / pairs : 0, p_sub = pairs > 0 ? threadIdx.x / pairs : 0;
+  const int p_id = pairs > 0 ? threadIdx.x % pairs : 0;
+  Pair pair{0, -1};
+  if (p_sub < n_sub) {
+    pair = pair_of(a, p_id);
+    if (p_sub == 0) turn_sm[p_id] = pair.axis >= 0;
   }
+  // the rows' side: this thread's chunk (or one of each half), share and token
+  const int c = threadIdx.x % g.n_chunks, u0 = threadIdx.x / g.n_chunks, h0 = u0 % g.lanes, tk = u0 / g.lanes;
+  const int pair_chunks = HALVES ? a.n_pairs >> 3 : g.n_chunks;
+  const bool both = c < pair_chunks;
+  const int e0 = both ? c * 8 : (c + pair_chunks) * 8;
+  const int gap = HALVES ? a.n_pairs : a.D >> 1;  // from the first chunk to the second
+  const int s0 = HALVES ? c * 8 : c * 4, s1 = HALVES ? s0 + 4 : s0 + (a.D >> 2);  // its pairs: s0 .. s0+3, s1 .. s1+3
+  const bool pair_chunk = a.rotate && both;
+  const int nq = a.q != nullptr ? a.H : 0;
 
-  int64_t k_off = -1, v_off = -1;
-  if (a.append) {
-    const bool report = c == 0 && h0 == 0;
-    const int len = clamped_length(a.cache, b, report);
-    const int n = clamped_new(a.cache, a.tok, b, len, report);
-    if (t < n) {
-      const int slot = len + t, page = page_of(a.cache, b, slot);
+  int buf = 0;
+  for (int row0 = blockIdx.x * g.tokens; row0 < rows; row0 += step, buf ^= 1) {
+    const int row = row0 + tk;
+    const bool on = tk < g.tokens && row < rows;
+    const int b = on ? row / a.T : 0, t = on ? row - b * a.T : 0;
+    // the token's rows: q heads, k heads, v heads (append), each with its head stride
+    const uint16_t *q_src = a.q + b * a.qs[0] + t * a.qs[1] + e0;
+    uint16_t *q_dst = a.qo + b * a.qos[0] + t * a.qos[1] + e0;
+    const uint16_t *k_src = a.k + b * a.ks[0] + t * a.ks[1] + e0, *v_src = nullptr;
+    uint16_t *k_dst = a.ko + b * a.kos[0] + t * a.kos[1] + e0, *v_dst = nullptr;
+    int n_heads = on ? g.n_heads : 0;
+    if (a.append && on) {
+      const bool report = c == 0 && h0 == 0;
+      const int len = clamped_length(a.cache, b, report);
+      const int n = clamped_new(a.cache, a.tok, b, len, report);
+      const int slot = len + t, page = t < n ? page_of(a.cache, b, slot) : -1;
       if (page >= 0) {
-        k_off = slot_offset(a.cache.ks, a.cache, page, slot, 0);
-        v_off = slot_offset(a.cache.vs, a.cache, page, slot, 0);
-      } else if (report) {
-        record_status(a.cache.status, BSA_ERR_BAD_CACHE);
+        k_dst = a.cache.k + slot_offset(a.cache.ks, a.cache, page, slot, 0) + e0;
+        v_dst = a.cache.v + slot_offset(a.cache.vs, a.cache, page, slot, 0) + e0;
+        v_src = a.v + b * a.vs[0] + t * a.vs[1] + e0;
+      } else {
+        n_heads = nq;  // a padding token, or a bad page: its q alone
+        if (report && t < n) record_status(a.cache.status, BSA_ERR_BAD_CACHE);
       }
     }
-  }
-
-  constexpr int U = 4;  // heads in flight
-  for (int h = h0; h < n_heads; h += U * head_split) {
-    HeadPtr hp[U];
+    const int64_t k_ds = a.append ? a.cache.ks[2] : a.kos[2], v_ds = a.append ? a.cache.vs[2] : 0;
+    auto src_of = [&](int i) {
+      return i < nq ? q_src + i * a.qs[2] : i < nq + a.H_kv ? k_src + (i - nq) * a.ks[2] : v_src + (i - nq - a.H_kv) * a.vs[2];
+    };
+    auto dst_of = [&](int i) {
+      return i < nq ? q_dst + i * a.qos[2] : i < nq + a.H_kv ? k_dst + (i - nq) * k_ds : v_dst + (i - nq - a.H_kv) * v_ds;
+    };
     int4 v0[U], v1[U];
+    auto load = [&](int h) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = h + u * head_split;
-      hp[u] = HeadPtr{nullptr, nullptr, false};
-      if (i < n_heads) hp[u] = head_ptr(a, i, b, t, k_off, v_off);
-      if (hp[u].dst != nullptr) {
-        v0[u] = *reinterpret_cast<const int4 *>(hp[u].src + e0);
-        if (both) v1[u] = *reinterpret_cast<const int4 *>(hp[u].src + e1);
+      for (int u = 0; u < U; ++u) {
+        const int i = h + u * g.lanes;
+        if (i < n_heads) {
+          const uint16_t *src = src_of(i);
+          v0[u] = *reinterpret_cast<const int4 *>(src);
+          if (both) v1[u] = *reinterpret_cast<const int4 *>(src + gap);
+        }
+      }
+    };
+    load(h0);  // in flight under the sines
+
+    float *cs_sm = trig + buf * 2 * g.tokens * pairs, *sn_sm = cs_sm + g.tokens * pairs;
+    if (p_sub < n_sub) {
+      for (int k = p_sub; k < g.tokens && row0 + k < rows; k += n_sub) {
+        const int bb = (row0 + k) / a.T;
+        float cv, sv;
+        turn_of(a, pair, bb, row0 + k - bb * a.T, cv, sv);
+        cs_sm[k * pairs + p_id] = cv;
+        sn_sm[k * pairs + p_id] = sv;
       }
     }
+    __syncthreads();  // one a step: the next one writes the other buffer
+    float cs[P], sn[P];
+    uint32_t rot = 0;
+    if (pair_chunk && on) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (hp[u].dst == nullptr) continue;
-      if (hp[u].turn && rot != 0u) {
-        if constexpr (HALVES) turn_halves<FP16>(v0[u], v1[u], cs, sn, rot);
-        else v0[u] = turn_interleaved<FP16>(v0[u], cs, sn, rot);
+      for (int i = 0; i < P; i += 4) {
+        const int at = i == 0 ? s0 : s1;
+        const float4 x = *reinterpret_cast<const float4 *>(cs_sm + tk * pairs + at);
+        const float4 y = *reinterpret_cast<const float4 *>(sn_sm + tk * pairs + at);
+        cs[i] = x.x, cs[i + 1] = x.y, cs[i + 2] = x.z, cs[i + 3] = x.w;
+        sn[i] = y.x, sn[i + 1] = y.y, sn[i + 2] = y.z, sn[i + 3] = y.w;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) rot |= static_cast<uint32_t>(turn_sm[at + k]) << (i + k);
       }
-      *reinterpret_cast<int4 *>(hp[u].dst + e0) = v0[u];
-      if (both) *reinterpret_cast<int4 *>(hp[u].dst + e1) = v1[u];
+    }
+    for (int h = h0; h < n_heads; h += U * g.lanes) {
+      if (h != h0) load(h);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = h + u * g.lanes;
+        if (i >= n_heads) continue;
+        if (rot != 0u && i < nq + a.H_kv) {
+          if constexpr (HALVES) {
+            turn_halves<FP16>(v0[u], v1[u], cs, sn, rot);
+          } else {
+            v0[u] = turn_interleaved<FP16>(v0[u], cs, sn, rot);
+            v1[u] = turn_interleaved<FP16>(v1[u], cs + 4, sn + 4, rot >> 4);
+          }
+        }
+        uint16_t *dst = dst_of(i);
+        *reinterpret_cast<int4 *>(dst) = v0[u];
+        if (both) *reinterpret_cast<int4 *>(dst + gap) = v1[u];
+      }
     }
   }
 }
 
 template <bool FP16, bool HALVES>
 cudaError_t launch(const RopeArgs &a, cudaStream_t s) {
-  const int n_heads = (a.q != nullptr ? a.H : 0) + (a.append ? 2 * a.H_kv : a.k != nullptr ? a.H_kv : 0);
-  const int chunks = HALVES ? a.D / 8 - a.n_pairs / 8 : a.D / 8;
+  RopeGrid g;
+  g.n_heads = (a.q != nullptr ? a.H : 0) + (a.append ? 2 * a.H_kv : a.k != nullptr ? a.H_kv : 0);
+  g.n_chunks = HALVES ? a.D / 8 - a.n_pairs / 8 : a.D / 16;
+  g.pairs = !a.rotate ? 0 : HALVES ? a.n_pairs : a.D / 2;
   const int64_t rows = static_cast<int64_t>(a.B) * a.T;
-  // heads shared out over threads until the GPU is full (148 SMs x 2048
-  // threads), at most 16 heads a thread
-  const int64_t full = 148 * 2048;
-  int64_t split = (full + rows * chunks - 1) / (rows * chunks);
-  split = std::max<int64_t>(split, (n_heads + 15) / 16);
-  split = std::min<int64_t>(split, n_heads);
-  const int64_t units = rows * chunks * split;
-  const int64_t blocks = (units + 255) / 256;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  // a thread takes about 20 heads (few waits for the sines a byte: 75600 tokens x
+  // 80 heads 508 us, with 8 heads 566) where there are tokens enough for four
+  // blocks an SM, else fewer tokens a block and fewer heads a thread
+  const int shares = 256 / g.n_chunks;
+  const int64_t few = (rows + 4 * 148 - 1) / (4 * 148);
+  g.tokens = static_cast<int>(std::min<int64_t>(few, shares / std::min(shares, (g.n_heads + 19) / 20)));
+  g.lanes = std::max(1, std::min(shares / g.tokens, g.n_heads));
+  const int64_t blocks = std::min<int64_t>((rows + g.tokens - 1) / g.tokens, 148 * 8);
   count_launch();
-  k_rope<FP16, HALVES><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a, n_heads, chunks, static_cast<int>(split));
+  k_rope<FP16, HALVES><<<static_cast<unsigned>(blocks), 256, (g.tokens * 16 + 1) * g.pairs, s>>>(a, g);
   return cudaGetLastError();
 }
 
