@@ -617,7 +617,8 @@ template <bool FP16, int D, int NX>
 cudaError_t launch(const AttendParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t s) {
   using L = AttendSmem<D, NX>;
   static_assert(L::kAlloc <= 232448, "shared memory of one CTA");
-  cudaError_t e = cudaFuncSetAttribute(k_attend<FP16, D, NX>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(k_attend<FP16, D, NX>, L::kAlloc, done);
   if (e != cudaSuccess) return e;
   count_launch(2);
   k_attend<FP16, D, NX><<<ctas, 384, L::kAlloc, s>>>(tk, tv, p);

@@ -368,10 +368,8 @@ cudaError_t select(const EvictArgs &a, int heads, int ctas, cudaStream_t s) {
   const int share = ((a.cache.capacity + 31) / 32 + ctas * kWarps - 1) / (ctas * kWarps) * THREADS;
   const int key_cap = K == 0 && share <= kMaxKeys ? share : 0;
   cudaError_t e = cudaSuccess;
-  if (K == 0 &&
-      (e = cudaFuncSetAttribute(k_evict_select<THREADS, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4)) !=
-          cudaSuccess)
-    return e;
+  static std::atomic<uint64_t> done{0};
+  if (K == 0 && (e = allow_smem(k_evict_select<THREADS, K>, kMaxKeys * 4, done)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(heads) * ctas);
   cfg.blockDim = dim3(THREADS);

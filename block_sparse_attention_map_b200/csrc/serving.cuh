@@ -3,6 +3,7 @@
 #pragma once
 
 #include "internal.h"
+#include <atomic>
 #include <climits>
 
 #include "ptx.cuh"
@@ -73,6 +74,20 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 }
 
 // ---------------------------------------------------------------- launchers
+// Raises a kernel's limit of dynamic shared memory, once per device and kernel
+// (`done` is the caller's own word, a bit a device).
+template <typename F>
+cudaError_t allow_smem(F *kernel, int bytes, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (bit != 0 && (done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 struct RopeArgs {
   int B, T, H, H_kv, D;
   int n_axes, n_pairs, inverse, rotate;

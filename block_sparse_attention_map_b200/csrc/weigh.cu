@@ -289,7 +289,8 @@ template <bool FP16, int D>
 cudaError_t launch(const WeighParams &p, const CUtensorMap &tk, int ctas, cudaStream_t s) {
   using L = WeighSmem<D>;
   static_assert(L::kAlloc <= 232448, "shared memory of one CTA");
-  const cudaError_t e = cudaFuncSetAttribute(k_weigh<FP16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(k_weigh<FP16, D>, L::kAlloc, done);
   if (e != cudaSuccess) return e;
   count_launch();
   k_weigh<FP16, D><<<ctas, 128 + kSumThreads, L::kAlloc, s>>>(tk, p);
