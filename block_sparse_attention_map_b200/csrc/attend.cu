@@ -19,12 +19,15 @@
 //               the S columns).
 //   warps 4-7, 8-11   two softmax groups, one row a thread with its 128 scores in
 //               registers (224 a thread, from the other warps' share): the tile's
-//               maximum, lazy rescale of O, P as 16-bit.  NX = 1: the groups take
+//               maximum, lazy rescale of O, P as 16-bit.  Where the piece has two
+//               row tiles, each group has one; where it has one, the groups take
 //               the key tiles in turn, each with its own running maximum, sums and
 //               O, and add the two up in the epilogue, each for half the columns
 //               (one group alone left the tensor and load pipes waiting for its
-//               chain of latencies: 187 -> 141 us, 16 sequences x 32 tokens x 4
-//               heads a group over 33002 keys).  NX = 2: a group a row tile.
+//               chain of latencies: 187 -> 148 us, 16 sequences x 32 tokens x 4
+//               heads a group over 33002 keys; key tiles taken as two halves, to
+//               overlap more, spent more on the barriers: 182 against 148 us at
+//               24000 keys).
 // V of what no row may see: slots past the new tokens are zeroed in shared memory
 // (0 * NaN is NaN in the product), and a new token's infinities and NaN are taken
 // out of the tile and added back in the epilogue of the rows that see the token.
@@ -36,6 +39,10 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// Up to this capacity a CTA takes its rows' whole sequence, padding rows too, and
+// nothing is joined: four key tiles one after the other take less than a second
+// launch (2 heads, 7 tokens, 250 keys: 10.8 us with it).
+constexpr int kWholeSlots = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: tolerate p up to 2^8
 
 struct AttendParams {
@@ -57,12 +64,15 @@ struct AttendSmem {
   static constexpr int NK = D == 128 ? 3 : 5, NV = D == 128 ? (NX == 1 ? 3 : 2) : 5;
   static constexpr int kQ = 0, kK = NX * kTB, kV = kK + NK * kTB, kBar = kV + NV * kTB;
   static constexpr int bKFull = 0, bKEmpty = NK, bVFull = 2 * NK, bVEmpty = bVFull + NV, bQFull = bVEmpty + NV,
-                       bSFull = bQFull + NX, bPFull = bSFull + 2, bPVDone = bPFull + 2, bFinal = bPVDone + 2,
+                       bSFull = bQFull + 1, bPFull = bSFull + 2, bPVDone = bPFull + 2, bQEmpty = bPVDone + 2,
+                       bFinal = bQEmpty + 1,
                        kNumBars = bFinal + 1;
   static constexpr int kBad = kBar + kNumBars * 8;     // uint32 [4][2]: new tokens whose V is not finite
   static constexpr int kRun = kBad + 32;               // RunStart
   static constexpr int kMisc = kRun + 16;              // tmem slot, abort flag
-  static constexpr int kAlloc = kMisc + 16;
+  // for the other group, where the groups take the key tiles in turn: maximum and rounded sum of group 0's rows; maximum, sum and rounded sum of group 1's
+  static constexpr int kSums = kMisc + 16;
+  static constexpr int kAlloc = kSums + 5 * kTile * 4;
 };
 
 // Mask of the 16-bit halves of `w` that are infinite or NaN.
@@ -72,7 +82,7 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   return ((w & e) == e ? 0xffffu : 0u) | ((w & (e << 16)) == (e << 16) ? 0xffff0000u : 0u);
 }
 
-template <bool FP16, int D, int NX>
+template <bool FP16, int D, int NX, bool WHOLE>
 __global__ void __launch_bounds__(384, 1)
 k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttendParams p) {
   using L = AttendSmem<D, NX>;
@@ -87,7 +97,7 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
 
   if (threadIdx.x == 32) {
     for (int i = 0; i < L::kNumBars; ++i)
-      mbar_init(&bars[i], i >= L::bQFull && i < L::bQFull + NX ? 256 / NX : i >= L::bPFull && i < L::bPFull + 2 ? 128 : 1);
+      mbar_init(&bars[i], i == L::bQFull ? 256 : i >= L::bPFull && i < L::bPFull + 2 ? 128 : 1);
     *abort_flag = 0;
     for (int i = 0; i < 8; ++i) bad[i] = 0;
     fence_mbar_init();
@@ -98,7 +108,7 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
       tma_prefetch_desc(&tk);
       tma_prefetch_desc(&tv);
     }
-    const RunStart r = find_run<kTile * NX>(p.cache, p.tok, lane);
+    const RunStart r = find_run<kTile * NX, WHOLE>(p.cache, p.tok, lane);
     if (lane == 0) *run_sm = r;
   }
   if (warp == 1) {
@@ -109,13 +119,17 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_trigger();
+  if (!WHOLE) pdl_trigger();
   const uint32_t tmem = *tmem_slot;
   Watchdog wd{abort_flag, p.cache.status, kWaitLimitNs};
   const RunStart run = *run_sm;
   if (threadIdx.x == 0 && (smem_u32(sm) & 1023u) != 0u) wd.trip(BSA_ERR_UNSUPPORTED);
   __syncthreads();
 
+  // row tiles of a piece with rows in them
+  auto row_tiles = [&](const Walk<kTile * NX, WHOLE> &w) {
+    return NX == 1 || w.s.n * p.tok.G - w.rg * kTile * NX <= kTile ? 1 : 2;
+  };
   constexpr uint32_t kIdescS = FP16 ? idesc_f16_f32(128, 128, 0, 0) : idesc_bf16_f32(128, 128, 0, 0);
   constexpr uint32_t kIdescPV = FP16 ? idesc_f16_f32(128, D, 0, 1) : idesc_bf16_f32(128, D, 0, 1);
 
@@ -125,7 +139,7 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
   if (wd.aborted()) {
   } else if (warp == 0) {
     // ------------------------------------------------------------ producer
-    Walk<kTile * NX> w(p.cache, p.tok, run);
+    Walk<kTile * NX, WHOLE> w(p.cache, p.tok, run);
     uint32_t kv = 0;
     bool stop = false;
     const int boxes = kTile >> p.box_log;
@@ -171,15 +185,14 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      Walk<kTile * NX> w(p.cache, p.tok, run);
-      uint32_t kv = 0, used[2] = {0, 0};  // key tiles done; tiles each group has had
+      Walk<kTile * NX, WHOLE> w(p.cache, p.tok, run);
+      uint32_t kv = 0, used0 = 0, used1 = 0;  // key tiles done; tiles each group has had
       bool stop = false;
-      // S_x = Q K^T of key tile number i for group x
-      auto issue_s = [&](int x, uint32_t i) -> bool {
+      // S_x = Q_q K^T of key tile number i
+      auto issue_s = [&](int x, int q, uint32_t i) -> bool {
         if (!wd.wait(&bars[L::bKFull + i % NK], (i / NK) & 1)) return false;
         tc_fence_after();
-        const uint32_t q_addr = smem_u32(sm + L::kQ + (NX == 1 ? 0 : x) * kTB);
-        const uint32_t k_addr = smem_u32(sm + L::kK + (i % NK) * kTB);
+        const uint32_t q_addr = smem_u32(sm + L::kQ + q * kTB), k_addr = smem_u32(sm + L::kK + (i % NK) * kTB);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
@@ -191,8 +204,8 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
       };
       // O_x += P_x V of key tile number i
       auto issue_pv = [&](int x, uint32_t i, bool first) -> bool {
-        if (!wd.wait(&bars[L::bPFull + x], used[x] & 1)) return false;
-        ++used[x];
+        if (!wd.wait(&bars[L::bPFull + x], (x == 0 ? used0 : used1) & 1)) return false;
+        (x == 0 ? used0 : used1) += 1;
         tc_fence_after();
         const uint32_t v_addr = smem_u32(sm + L::kV + (i % NV) * kTB);
 #pragma unroll
@@ -204,37 +217,41 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
       };
       while (!stop && w.next(p.cache, p.tok)) {
         const int nt = w.t1 - w.t0;
-        for (int x = 0; x < NX && !stop; ++x) stop = !wd.wait(&bars[L::bQFull + x], w.index & 1);
-        if (stop) break;
+        if (!wd.wait(&bars[L::bQFull], w.index & 1)) break;
         tc_fence_after();
-        // an S follows the PV that reads P from its columns in issue order, so needs no wait for it
-        if constexpr (NX == 1) {
+        // an S follows the P V that reads P from its columns in issue order, so needs no wait for it
+        if (row_tiles(w) == 1) {
           for (int j = 0; j < min(nt, 2) && !stop; ++j) {
-            stop = !issue_s((kv + j) & 1, kv + j);
+            stop = !issue_s((kv + j) & 1, 0, kv + j);
             if (!stop) mma_commit(&bars[L::bKEmpty + (kv + j) % NK]);
           }
+          if (nt <= 2) mma_commit(&bars[L::bQEmpty]);
           for (int j = 0; j < nt && !stop; ++j, ++kv) {
             if (!wd.wait(&bars[L::bVFull + kv % NV], (kv / NV) & 1)) { stop = true; break; }
             if (!issue_pv(kv & 1, kv, j < 2)) { stop = true; break; }
             mma_commit(&bars[L::bVEmpty + kv % NV]);
             if (j + 2 < nt) {
-              if (!issue_s(kv & 1, kv + 2)) { stop = true; break; }
+              if (!issue_s(kv & 1, 0, kv + 2)) { stop = true; break; }
               mma_commit(&bars[L::bKEmpty + (kv + 2) % NK]);
             }
+            // the piece's last S is issued: Q's shared memory is free once it is done
+            if (nt > 2 && j + 3 == nt) mma_commit(&bars[L::bQEmpty]);
           }
         } else {
-          for (int x = 0; x < 2 && !stop; ++x) stop = !issue_s(x, kv);
+          for (int x = 0; x < 2 && !stop && nt > 0; ++x) stop = !issue_s(x, x, kv);
           if (stop) break;
-          mma_commit(&bars[L::bKEmpty + kv % NK]);
+          if (nt > 0) mma_commit(&bars[L::bKEmpty + kv % NK]);
+          if (nt <= 1) mma_commit(&bars[L::bQEmpty]);
           for (int j = 0; j < nt && !stop; ++j, ++kv) {
             if (!wd.wait(&bars[L::bVFull + kv % NV], (kv / NV) & 1)) { stop = true; break; }
             for (int x = 0; x < 2 && !stop; ++x) {
               stop = !issue_pv(x, kv, j == 0);
-              if (!stop && j + 1 < nt) stop = !issue_s(x, kv + 1);
+              if (!stop && j + 1 < nt) stop = !issue_s(x, x, kv + 1);
             }
             if (stop) break;
             mma_commit(&bars[L::bVEmpty + kv % NV]);
             if (j + 1 < nt) mma_commit(&bars[L::bKEmpty + (kv + 1) % NK]);
+            if (j + 2 == nt) mma_commit(&bars[L::bQEmpty]);
           }
         }
       }
@@ -254,11 +271,28 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
     auto wwait = [&](uint64_t *bar, uint32_t parity) {
       return __all_sync(0xffffffffu, wd.wait(bar, parity)) != 0;
     };
-    Walk<kTile * NX> w(p.cache, p.tok, run);
+    Walk<kTile * NX, WHOLE> w(p.cache, p.tok, run);
     uint32_t kv = 0, used = 0;  // key tiles of the run so far, and this group's among them
     bool stop = wd.aborted();
-    while (w.next(p.cache, p.tok)) {
-      const int row0 = (w.rg * NX + (NX == 1 ? 0 : x)) * kTile, rows = min(w.s.n * G - row0, kTile);
+    // a piece's Q rows -> shared memory, by both groups, 16 bytes a lane
+    auto load_q = [&](const Walk<kTile * NX, WHOLE> &n) {
+      const int row0 = n.rg * NX * kTile, rows = min(n.s.n * G - row0, kTile * NX);
+#pragma unroll 4
+      for (int i = threadIdx.x - 128; i < rows * kPieces; i += 256) {
+        const int rr = i / kPieces, c = i % kPieces, grow = row0 + rr;
+        const int4 v = *reinterpret_cast<const int4 *>(p.q + n.b * p.qs[0] + (grow / G) * p.qs[1] +
+                                                       (n.hk * G + grow % G) * p.qs[2] + c * 8);
+        *reinterpret_cast<int4 *>(sm + L::kQ + (rr >> 7) * kTB + (c >> 3) * 16384 + (rr & 127) * 128 +
+                                  (((c & 7) ^ (rr & 7)) << 4)) = v;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&bars[L::bQFull]);
+    };
+    bool more = w.next(p.cache, p.tok);
+    if (more && !stop) load_q(w);
+    while (more) {
+      const bool turns = row_tiles(w) == 1;  // the groups take the key tiles in turn; else each has a row tile
+      const int row0 = w.rg * NX * kTile + (turns ? 0 : x * kTile), rows = min(w.s.n * G - row0, kTile);
       const int row = row0 + r, tok = row / G, h = w.hk * G + row % G;
       const bool row_ok = r < rows, warp_on = quarter * 32 < rows;
       uint32_t *bad_w = bad + (w.index & 3) * 2;
@@ -266,22 +300,11 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
         bad[((w.index + 1) & 3) * 2] = 0;
         bad[((w.index + 1) & 3) * 2 + 1] = 0;
       }
-      // Q rows -> shared memory (every S of the piece before has read them), 16 bytes a lane
-#pragma unroll 4
-      for (int i = NX == 1 ? threadIdx.x - 128 : r; i < rows * kPieces; i += 256 / NX) {
-        const int rr = i / kPieces, c = i % kPieces, grow = row0 + rr;
-        const int4 v = *reinterpret_cast<const int4 *>(p.q + w.b * p.qs[0] + (grow / G) * p.qs[1] +
-                                                       (w.hk * G + grow % G) * p.qs[2] + c * 8);
-        *reinterpret_cast<int4 *>(sm + L::kQ + (NX == 1 ? 0 : x) * kTB + (c >> 3) * 16384 + rr * 128 +
-                                  (((c & 7) ^ (rr & 7)) << 4)) = v;
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(&bars[L::bQFull + (NX == 1 ? 0 : x)]);
       const uint64_t word = row_ok ? tree_word(p.tok, w.b, tok, w.s.n) : 0ull;
       float m_ref = -INFINITY, l = 0.f, l_r = 0.f;
 
       for (int t = w.t0; t < w.t1 && !stop; ++t, ++kv) {
-        if (NX == 1 && (kv & 1) != static_cast<uint32_t>(x)) continue;
+        if (turns && (kv & 1) != static_cast<uint32_t>(x)) continue;
         const int j0 = t * kTile;
         const bool edge = j0 + kTile > w.s.len;
         uint32_t allow[4] = {~0u, ~0u, ~0u, ~0u};
@@ -293,7 +316,7 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
             else if (d0 >= 0) allow[q] = static_cast<uint32_t>(word >> d0);
             else if (d0 > -32) allow[q] = static_cast<uint32_t>(word << -d0) | ((1u << -d0) - 1u);
           }
-          if (NX == 1 || x == 0) {
+          if (turns || x == 0) {
             // this thread's key: V past the new tokens becomes zero, what is not
             // finite in a new token's V is taken out
             if (!wwait(&bars[L::bVFull + kv % NV], (kv / NV) & 1)) { stop = true; break; }
@@ -301,7 +324,7 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
             const int d = j0 + r - w.s.len;
             if (d >= 0) {
               bool found = false;
-#pragma unroll 1
+#pragma unroll 8
               for (int c = 0; c < kPieces; ++c) {
                 int4 *q4 = reinterpret_cast<int4 *>(vrow + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4));
                 int4 v = make_int4(0, 0, 0, 0);
@@ -394,35 +417,38 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
         mbar_arrive(&bars[L::bPFull + x]);
         ++used;
       }
+      // the next piece's Q, so that its first S runs under this piece's epilogue
+      Walk<kTile * NX, WHOLE> next = w;
+      more = next.next(p.cache, p.tok);
+      if (more && !stop) {
+        if (wwait(&bars[L::bQEmpty], w.index & 1)) load_q(next);
+        else stop = true;
+      }
       // ---------------------------------------------------------- epilogue
       // (a group that has had no tile in the piece has nothing to wait for)
-      const bool had = NX == 2 || w.t1 - w.t0 > 1 || ((kv - 1) & 1) == static_cast<uint32_t>(x);
+      const int nt = w.t1 - w.t0;
+      const bool had = turns ? nt > 1 || (nt == 1 && ((kv - 1) & 1) == static_cast<uint32_t>(x)) : nt > 0;
       if (!stop && had && !wwait(&bars[L::bPVDone + x], (used - 1) & 1)) stop = true;
       tc_fence_after();
       float f_mine = 1.f, f_other = 0.f;
-      const bool both = NX == 1 && w.t1 - w.t0 > 1;
-      if constexpr (NX == 1) {
-        // the other group's maximum and sums, through this row's TMEM lane (its S columns are free)
-        if (!stop && both) {
-          uint32_t mine[8] = {__float_as_uint(m_ref), __float_as_uint(l), __float_as_uint(l_r), 0, 0, 0, 0, 0};
-          tmem_st8(t_s, mine);
-          tmem_wait_st();
-        }
+      const bool both = turns && nt > 1;
+      {
+        // the other group's maximum and sums, through shared memory
+        float *sums = reinterpret_cast<float *>(sm + L::kSums);
+        float *mine = sums + x * 2 * kTile, *other = sums + (x ^ 1) * 2 * kTile;
+        mine[r] = m_ref;
+        mine[kTile + r] = l_r;
+        if (x == 1) mine[2 * kTile + r] = l;
         tc_fence_before();
         named_bar_sync(1, 256);  // in every path, so that the two groups' barriers pair up
         tc_fence_after();
-        if (!stop && both) {
-          uint32_t other[16];
-          tmem_ld16(tmem + lane_off + (x ^ 1) * 128, other);
-          tmem_wait_ld();
-          const float mo = __uint_as_float(other[0]), M = fmaxf(m_ref, mo), Mu = M == -INFINITY ? 0.f : M;
+        if (both) {
+          const float mo = other[r], M = fmaxf(m_ref, mo), Mu = M == -INFINITY ? 0.f : M;
           f_mine = exp2f(m_ref - Mu);
           f_other = exp2f(mo - Mu);
-          l = f_mine * l + f_other * __uint_as_float(other[1]);
-          l_r = f_mine * l_r + f_other * __uint_as_float(other[2]);
+          if (x == 0) l = f_mine * l + f_other * other[2 * kTile + r];
+          l_r = f_mine * l_r + f_other * other[kTile + r];
           m_ref = M;
-        } else if (!had) {
-          // the piece's one tile was the other group's, which writes the rows
         }
       }
       if (!stop && warp_on && had) {
@@ -434,11 +460,11 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
         uint16_t *orow = p.out + w.b * p.os[0] + tok * p.os[1] + h * p.os[2];
         // a piece that starts this CTA's run goes to slot 0, one that ends it to slot 1
         const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (w.index > 0 ? 1 : 0)) * (kTile * NX) +
-                             (NX == 1 ? 0 : x) * kTile + r;
+                             (turns ? 0 : x * kTile) + r;
         float *prow = p.part_o + part * D;
         // the columns [c0, c1) * 16: half of them where both groups hold a part of the row
         const int c0 = both ? x * (D / 32) : 0, c1 = both ? c0 + D / 32 : D / 16;
-#pragma unroll 1
+#pragma unroll 2
         for (int c = c0; c < c1; ++c) {
           uint32_t o[16];
           tmem_ld16(t_o + c * 16, o);
@@ -495,9 +521,20 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
           else p.part_ml[part] = make_float4(m_ref, l, l_r, 0.f);
         }
       }
+      // padding rows: those of this group's row tile, and of the other one where no row of it is real
+      const int last = turns && NX == 2 && x == 1 ? kTile : 0;
+      if (WHOLE && (turns ? x == 0 || NX == 2 : true) && row + last >= w.s.n * G && row + last < p.tok.T * G) {
+        const int tok = (row + last) / G, h = w.hk * G + (row + last) % G;
+        uint16_t *orow = p.out + w.b * p.os[0] + tok * p.os[1] + h * p.os[2];
+#pragma unroll 1
+        for (int c = 0; c < D / 8; ++c) reinterpret_cast<int4 *>(orow)[c] = make_int4(0, 0, 0, 0);
+        p.lse[(static_cast<int64_t>(w.b) * p.tok.H + h) * p.tok.T + tok] = -INFINITY;
+      }
       tc_fence_before();
       __syncwarp();
-      if (stop) break;
+      // both groups have read both O's (and the sums) before either's next product writes them
+      named_bar_sync(2, 256);
+      w = next;
     }
   }
 
@@ -617,14 +654,23 @@ template <bool FP16, int D, int NX>
 cudaError_t launch(const AttendParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t s) {
   using L = AttendSmem<D, NX>;
   static_assert(L::kAlloc <= 232448, "shared memory of one CTA");
+  const int64_t items = static_cast<int64_t>(p.cache.B) * p.cache.H_kv * ((p.tok.T * p.tok.G + kTile * NX - 1) / (kTile * NX));
+  if (p.cache.capacity <= kWholeSlots) {
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(k_attend<FP16, D, NX, true>, L::kAlloc, done);
+    if (e != cudaSuccess) return e;
+    count_launch();
+    k_attend<FP16, D, NX, true>
+        <<<static_cast<unsigned>(std::min<int64_t>(items, ctas)), 384, L::kAlloc, s>>>(tk, tv, p);
+    return cudaGetLastError();
+  }
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(k_attend<FP16, D, NX>, L::kAlloc, done);
+  cudaError_t e = allow_smem(k_attend<FP16, D, NX, false>, L::kAlloc, done);
   if (e != cudaSuccess) return e;
   count_launch(2);
-  k_attend<FP16, D, NX><<<ctas, 384, L::kAlloc, s>>>(tk, tv, p);
+  k_attend<FP16, D, NX, false><<<ctas, 384, L::kAlloc, s>>>(tk, tv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // an item's tiles lie in about ctas / items runs, a few more where lengths differ
-  const int64_t items = static_cast<int64_t>(p.cache.B) * p.cache.H_kv * ((p.tok.T * p.tok.G + kTile * NX - 1) / (kTile * NX));
   return ctas > 8 * items ? join<FP16, D, NX, 8>(p, ctas, s) : join<FP16, D, NX, 1>(p, ctas, s);
 }
 
