@@ -108,6 +108,7 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
       tma_prefetch_desc(&tk);
       tma_prefetch_desc(&tv);
     }
+    pdl_wait();  // everything before this may run under the stream's preceding kernel
     const RunStart r = find_run<kTile * NX, WHOLE>(p.cache, p.tok, lane);
     if (lane == 0) *run_sm = r;
   }
@@ -119,7 +120,8 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (!WHOLE) pdl_trigger();
+  pdl_wait();
+  pdl_trigger();
   const uint32_t tmem = *tmem_slot;
   Watchdog wd{abort_flag, p.cache.status, kWaitLimitNs};
   const RunStart run = *run_sm;
@@ -660,16 +662,14 @@ cudaError_t launch(const AttendParams &p, const CUtensorMap &tk, const CUtensorM
     const cudaError_t e = allow_smem(k_attend<FP16, D, NX, true>, L::kAlloc, done);
     if (e != cudaSuccess) return e;
     count_launch();
-    k_attend<FP16, D, NX, true>
-        <<<static_cast<unsigned>(std::min<int64_t>(items, ctas)), 384, L::kAlloc, s>>>(tk, tv, p);
-    return cudaGetLastError();
+    return launch_pdl(k_attend<FP16, D, NX, true>, dim3(static_cast<unsigned>(std::min<int64_t>(items, ctas))), dim3(384),
+                      L::kAlloc, s, tk, tv, p);
   }
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(k_attend<FP16, D, NX, false>, L::kAlloc, done);
   if (e != cudaSuccess) return e;
   count_launch(2);
-  k_attend<FP16, D, NX, false><<<ctas, 384, L::kAlloc, s>>>(tk, tv, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_pdl(k_attend<FP16, D, NX, false>, dim3(ctas), dim3(384), L::kAlloc, s, tk, tv, p)) != cudaSuccess) return e;
   // an item's tiles lie in about ctas / items runs, a few more where lengths differ
   return ctas > 8 * items ? join<FP16, D, NX, 8>(p, ctas, s) : join<FP16, D, NX, 1>(p, ctas, s);
 }

@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) k_evict_selec
   const int head = blockIdx.x / ctas, b = head / a.cache.H_kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t base = static_cast<int64_t>(head) * a.cache.capacity;
+  pdl_wait();
   const int n = clamped_length(a.cache, b, tid == 0 && rank == 0);
   const float *score = a.score_in + base;
   const int32_t *pos = a.pos_in + base;
@@ -316,6 +317,7 @@ __global__ void __launch_bounds__(256) k_evict_move(const EvictArgs a, int per_h
   const int b = head / a.cache.H_kv, hk = head % a.cache.H_kv;
   const int sub = threadIdx.x % L, grp = threadIdx.x / L;
   pdl_wait();
+  pdl_trigger();
   // the block's moves of a step lie next to each other (rows of one DRAM page: 74 us with the groups' moves apart)
   const int m = a.count[head];
   const int64_t lb = static_cast<int64_t>(head) * a.list_cap, base = static_cast<int64_t>(head) * a.cache.capacity;
@@ -375,13 +377,15 @@ cudaError_t select(const EvictArgs &a, int heads, int ctas, cudaStream_t s) {
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = static_cast<size_t>(key_cap) * 4;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   count_launch(2);
   return cudaLaunchKernelEx(&cfg, k_evict_select<THREADS, K>, a, key_cap);
 }

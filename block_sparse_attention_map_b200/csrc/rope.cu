@@ -100,6 +100,8 @@ __global__ void __launch_bounds__(256, 4) k_rope(const RopeArgs a, const RopeGri
   uint8_t *turn_sm = reinterpret_cast<uint8_t *>(trig + 4 * g.tokens * pairs);
   const int rows = a.B * a.T, step = gridDim.x * g.tokens;  // rows < 2^31
 
+  pdl_wait();
+  pdl_trigger();
   // the sines' side: this thread's pair, and every n_sub-th token of a step
   const int n_sub = pairs > 0 ? 256 / pairs : 0, p_sub = pairs > 0 ? threadIdx.x / pairs : 0;
   const int p_id = pairs > 0 ? threadIdx.x % pairs : 0;
@@ -227,8 +229,7 @@ cudaError_t launch(const RopeArgs &a, cudaStream_t s) {
   g.lanes = std::max(1, std::min(shares / g.tokens, g.n_heads));
   const int64_t blocks = std::min<int64_t>((rows + g.tokens - 1) / g.tokens, 148 * 8);
   count_launch();
-  k_rope<FP16, HALVES><<<static_cast<unsigned>(blocks), 256, (g.tokens * 16 + 1) * g.pairs, s>>>(a, g);
-  return cudaGetLastError();
+  return launch_pdl(k_rope<FP16, HALVES>, dim3(static_cast<unsigned>(blocks)), dim3(256), (g.tokens * 16 + 1) * g.pairs, s, a, g);
 }
 
 }  // namespace

@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(128 + kSumThreads, 1) k_weigh(const __grid_con
   }
   if (warp == 0) {
     if (lane == 0) tma_prefetch_desc(&tk);
+    pdl_wait();  // everything before this may run under the stream's preceding kernel
     const RunStart r = find_run<kAllRows>(p.cache, p.tok, lane);
     if (lane == 0) *run_sm = r;
   }
@@ -87,6 +88,8 @@ __global__ void __launch_bounds__(128 + kSumThreads, 1) k_weigh(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait();
+  pdl_trigger();
   const uint32_t tmem = *tmem_slot;
   Watchdog wd{abort_flag, p.cache.status, kWaitLimitNs};
   const RunStart run = *run_sm;
@@ -293,8 +296,7 @@ cudaError_t launch(const WeighParams &p, const CUtensorMap &tk, int ctas, cudaSt
   const cudaError_t e = allow_smem(k_weigh<FP16, D>, L::kAlloc, done);
   if (e != cudaSuccess) return e;
   count_launch();
-  k_weigh<FP16, D><<<ctas, 128 + kSumThreads, L::kAlloc, s>>>(tk, p);
-  return cudaGetLastError();
+  return launch_pdl(k_weigh<FP16, D>, dim3(ctas), dim3(128 + kSumThreads), L::kAlloc, s, tk, p);
 }
 
 }  // namespace
