@@ -144,69 +144,87 @@ def _rope_layout(B, T, shape, stride, n, layout, inverse):
     return r
 
 
-def _rope_spec(B, T, index, pos, inv_freq, axis, layout, inverse):
-    ps, pt, n = pos.shape, pos.stride(), inv_freq.numel()
-    proto = _layout(("r", B, T, ps, pt, n, layout, inverse), lambda: _rope_layout(B, T, ps, pt, n, layout, inverse))
+def _check_tables(pos, inv_freq, axis, index):
+    """The rotation's tensors, but for the shape of ``pos``."""
     if pos.dtype != torch.int32 or pos.get_device() != index:
         raise ValueError(f"pos: expected an int32 tensor on cuda:{index}")
+    if inv_freq.dtype != torch.float64 or inv_freq.get_device() != index or not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq: expected a contiguous float64 tensor on cuda:{index}")
+    if axis.dtype != torch.int32 or axis.get_device() != index or not axis.is_contiguous():
+        raise ValueError(f"axis: expected a contiguous int32 tensor on cuda:{index}")
+
+
+def _rope_args(proto, pos, inv_freq, axis):
     r = RopeSpec.from_buffer_copy(proto)
-    r.inv_freq = _flat(inv_freq, "inv_freq", index, torch.float64, (n,))
-    r.axis = _flat(axis, "axis", index, torch.int32, (n,))
-    r.pos = pos.data_ptr()
+    r.inv_freq, r.axis, r.pos = inv_freq.data_ptr(), axis.data_ptr(), pos.data_ptr()
     return r
 
 
-def _check_apart(x, xs, out, os, span_x, span_out, name):
-    """``out`` is ``x`` itself or shares no memory with it."""
-    a, b, e = x.data_ptr(), out.data_ptr(), x.element_size()
-    if a < b + span_out * e and b < a + span_x * e and not (a == b and xs == os):
+def _check_apart(a, b, same, span_x, span_out, name):
+    """An output at address ``b`` is its input at ``a`` itself (``same`` strides) or shares no memory with it."""
+    if a < b + 2 * span_out and b < a + 2 * span_x and not (a == b and same):
         raise ValueError(f"{name}: overlaps its input without being it")
 
 
 def _pair_layout(xs, xt, os, ot, name):
-    """Strides and spans of a rotation's input and output."""
-    if os != xs:
-        raise ValueError(f"{name}_out: expected the input's shape {tuple(xs)}")
-    return _strides(xs, xt, name), _strides(os, ot, name + "_out"), _span(xs, xt), _span(os, ot)
+    """A rotation's input and output: (strides, output's strides, whether they are alike, spans)."""
+    if len(xs) != 4 or os != xs:
+        raise ValueError(f"{name} and {name}_out: expected [B, S, H, D] tensors of one shape")
+    return _strides(xs, xt, name), _strides(os, ot, name + "_out"), xt == ot, _span(xs, xt), _span(os, ot)
 
 
-def _pair(x, out, name, index, dtype):
-    """A rotation's input and output (new where None), checked: (out, their layout)."""
-    _rows(x, name, index, dtype)
-    if out is None:
-        out = torch.empty(x.shape, dtype=dtype, device=x.device)
-    _rows(out, name + "_out", index, dtype)
-    xs, xt, os, ot = x.shape, x.stride(), out.shape, out.stride()
-    lay = _layout(("p", xs, xt, os, ot), lambda: _pair_layout(xs, xt, os, ot, name))
-    _check_apart(x, xt, out, ot, lay[2], lay[3], name + "_out")
-    return out, lay
+def _rotate_layout(qs, qt, qos, qot, ks, kt, kos, kot, ps, pt, fs, axs, dtype, layout, inverse):
+    """A rotation's argument blocks, but for the addresses, and its inputs' and outputs' spans."""
+    xs = qs if qs is not None else ks
+    if len(xs) != 4:
+        raise ValueError("q and k are [B, S, H, D] tensors")
+    B, S, H, D = xs
+    t = Tokens(B, S, H, 0, D, dtype)
+    q = k = None
+    if qs is not None:
+        q = _pair_layout(qs, qt, qos, qot, "q")
+        t.q_stride[:], t.qo_stride[:] = q[0], q[1]
+    if ks is not None:
+        k = _pair_layout(ks, kt, kos, kot, "k")
+        if ks[0] != B or ks[1] != S or ks[3] != D:
+            raise ValueError("q and k must share B, S and D")
+        t.H_kv = ks[2]
+        t.k_stride[:], t.ko_stride[:] = k[0], k[1]
+    if len(fs) != 1 or axs != fs:
+        raise ValueError("inv_freq and axis: expected one entry a pair")
+    return t, _rope_layout(B, S, ps, pt, fs[0], layout, inverse), q and q[2:], k and k[2:]
 
 
 def _rotate(q, k, pos, inv_freq, axis, layout, inverse, q_out, k_out):
     x = q if q is not None else k
     if x is None:
         raise ValueError("give q, k or both")
-    dtype = DTYPE.get(x.dtype)
-    if not x.is_cuda or x.dim() != 4 or dtype is None:
+    kind, index = x.dtype, x.get_device()
+    if index < 0 or kind not in DTYPE:
         raise ValueError("q and k are [B, S, H, D] bf16 or fp16 CUDA tensors")
-    index = x.get_device()
-    B, S, H, D = x.shape
-    t = Tokens(B, S, H, 0, D, dtype)
-    qp = qop = kp = kop = None
+    qs = qt = qos = qot = ks = kt = kos = kot = qp = qop = kp = kop = None
+    for y in (q, k, q_out, k_out):
+        if y is not None and (y.dtype != kind or y.get_device() != index):
+            raise ValueError(f"q, k and their outputs: expected {kind} tensors on cuda:{index}")
+    _check_tables(pos, inv_freq, axis, index)
     if q is not None:
-        q_out, lay = _pair(q, q_out, "q", index, x.dtype)
-        t.q_stride[:], t.qo_stride[:] = lay[0], lay[1]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=kind, device=q.device)
+        qs, qt, qos, qot = q.shape, q.stride(), q_out.shape, q_out.stride()
         qp, qop = q.data_ptr(), q_out.data_ptr()
     if k is not None:
-        k_out, lay = _pair(k, k_out, "k", index, x.dtype)
-        ks = k.shape
-        if ks[0] != B or ks[1] != S or ks[3] != D:
-            raise ValueError("q and k must share B, S and D")
-        t.H_kv = ks[2]
-        t.k_stride[:], t.ko_stride[:] = lay[0], lay[1]
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=kind, device=k.device)
+        ks, kt, kos, kot = k.shape, k.stride(), k_out.shape, k_out.stride()
         kp, kop = k.data_ptr(), k_out.data_ptr()
-    r = _rope_spec(B, S, index, pos, inv_freq, axis, layout, inverse)
-    _call("bsa_rope", index, t, r, qp, qop, kp, kop)
+    args = (qs, qt, qos, qot, ks, kt, kos, kot, pos.shape, pos.stride(), inv_freq.shape, axis.shape, DTYPE[kind], layout,
+            inverse)
+    t, r, qa, ka = _layout(args, lambda: _rotate_layout(*args))
+    if qa is not None:
+        _check_apart(qp, qop, *qa, "q_out")
+    if ka is not None:
+        _check_apart(kp, kop, *ka, "k_out")
+    _call("bsa_rope", index, t, _rope_args(r, pos, inv_freq, axis), qp, qop, kp, kop)
     return q_out, k_out
 
 
@@ -247,6 +265,27 @@ def tree_words(parents):
     return torch.tensor(signed, dtype=torch.int64, device=parents.device).view(B, T)
 
 
+def _append_layout(ks, kt, vs, vt, qs, qt, qos, qot, ps, pt, fs, axs, layout, B, H_kv, D, dtype):
+    """An append's argument blocks, but for the addresses, and the spans of q and its output."""
+    if len(ks) != 4 or ks[0] != B or ks[2] != H_kv or ks[3] != D or vs != ks:
+        raise ValueError(f"k and v: expected [{B}, T, {H_kv}, {D}]")
+    T = ks[1]
+    t = Tokens(B, T, H_kv, H_kv, D, dtype)
+    t.k_stride[:], t.v_stride[:] = _strides(ks, kt, "k"), _strides(vs, vt, "v")
+    q = r = None
+    if qs is not None:
+        q = _pair_layout(qs, qt, qos, qot, "q")
+        if qs[0] != B or qs[1] != T or qs[3] != D:
+            raise ValueError("q must be [B, T, H, D] of the same tokens")
+        t.H = qs[2]
+        t.q_stride[:], t.qo_stride[:] = q[0], q[1]
+    if ps is not None:
+        if len(fs) != 1 or axs != fs:
+            raise ValueError("inv_freq and axis: expected one entry a pair")
+        r = _rope_layout(B, T, ps, pt, fs[0], layout, False)
+    return t, r, q and q[2:]
+
+
 class PagedCache:
     """A paged key/value cache and the calls around it.
 
@@ -282,7 +321,7 @@ class PagedCache:
         c.page_table = page_table.data_ptr()
         c.table_stride = page_table.stride(0) if self.B > 1 else 0
         c.length = _flat(length, "length", self._index, torch.int32, (self.B,))
-        self._ws = None
+        self._ws, self._sized = None, set()  # budgets the workspace holds
         self._workspace(0)
 
     def _workspace(self, budget):
@@ -319,14 +358,11 @@ class PagedCache:
             lambda: self._token_layout(shape, stride, out_shape, out_stride, scale)))
         if q.dtype != self.dtype or q.get_device() != self._index:
             raise ValueError(f"q: expected a {self.dtype} tensor on cuda:{self._index}")
-        self._options(t, shape[0], shape[1], tree, n_new)
-        return t
-
-    def _options(self, t, B, T, tree, n_new):
         if n_new is not None:
-            t.n_new = _flat(n_new, "n_new", self._index, torch.int32, (B,))
+            t.n_new = _flat(n_new, "n_new", self._index, torch.int32, (self.B,))
         if tree is not None:
-            t.tree = _flat(tree, "tree", self._index, torch.int64, (B, T))
+            t.tree = _flat(tree, "tree", self._index, torch.int64, shape[:2])
+        return t
 
     def append(self, k, v, q=None, rope=None, n_new=None, q_out=None):
         """The new tokens' k and v [B, T, H_kv, D] into the slots from
@@ -334,31 +370,31 @@ class PagedCache:
         axis, layout) rotates k on its way and q [B, T, H, D], which is returned
         (in ``q_out``).  ``n_new`` int32 [B]: only the first n_new[b] tokens of a
         sequence are stored."""
-        _rows(k, "k", self._index, self.dtype)
-        _rows(v, "v", self._index, self.dtype)
-        ks, vs = k.shape, v.shape
-        if ks[2] != self.H_kv or ks[3] != self.D or vs != ks or ks[0] != self.B:
-            raise ValueError(f"k and v: expected [{self.B}, T, {self.H_kv}, {self.D}]")
-        kt, vt = k.stride(), v.stride()
-        B, T = ks[0], ks[1]
-        t = Tokens(B, T, self.H_kv, self.H_kv, self.D, self._c.dtype)
-        t.k_stride[:], t.v_stride[:] = _layout(("kv", ks, kt, vt), lambda: (_strides(ks, kt, "k"), _strides(vs, vt, "v")))
-        self._options(t, B, T, None, n_new)
-        qp = qop = None
+        index, kind = self._index, self.dtype
+        for y in (k, v, q, q_out):
+            if y is not None and (y.dtype != kind or y.get_device() != index):
+                raise ValueError(f"k, v, q and q_out: expected {kind} tensors on cuda:{index}")
+        qs = qt = qos = qot = ps = pt = fs = axs = layout = qp = qop = r = None
         if q is not None:
-            q_out, lay = _pair(q, q_out, "q", self._index, self.dtype)
-            qs = q.shape
-            if qs[0] != B or qs[1] != T or qs[3] != self.D:
-                raise ValueError("q must be [B, T, H, D] of the same tokens")
-            t.H = qs[2]
-            t.q_stride[:], t.qo_stride[:] = lay[0], lay[1]
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=kind, device=self.device)
+            qs, qt, qos, qot = q.shape, q.stride(), q_out.shape, q_out.stride()
             qp, qop = q.data_ptr(), q_out.data_ptr()
-        r = None
         if rope is not None:
             pos, inv_freq, axis, layout = rope
-            r = _rope_spec(B, T, self._index, pos, inv_freq, axis, layout, False)
-        _call("bsa_cache_append", self._index, self._c, t, r, qp, qop, k.data_ptr(), v.data_ptr(), self._ws_ptr,
-              self._ws_bytes)
+            _check_tables(pos, inv_freq, axis, index)
+            ps, pt, fs, axs = pos.shape, pos.stride(), inv_freq.shape, axis.shape
+        args = (k.shape, k.stride(), v.shape, v.stride(), qs, qt, qos, qot, ps, pt, fs, axs, layout, self.B, self.H_kv, self.D,
+                self._c.dtype)
+        proto, rp, qa = _layout(args, lambda: _append_layout(*args))
+        t = Tokens.from_buffer_copy(proto)
+        if n_new is not None:
+            t.n_new = _flat(n_new, "n_new", index, torch.int32, (self.B,))
+        if qa is not None:
+            _check_apart(qp, qop, *qa, "q_out")
+        if rp is not None:
+            r = _rope_args(rp, pos, inv_freq, axis)
+        _call("bsa_cache_append", index, self._c, t, r, qp, qop, k.data_ptr(), v.data_ptr(), self._ws_ptr, self._ws_bytes)
         return q_out
 
     def attend(self, q, tree=None, n_new=None, scale=None, out=None, lse=None):
@@ -414,8 +450,9 @@ class PagedCache:
         e.score_out = e.score_in if scores_out is scores else _flat(scores_out, "scores_out", index, torch.float32, shape)
         e.pos_out = e.pos_in if pos_out is pos else _flat(pos_out, "pos_out", index, torch.int32, shape)
         e.length_out = _flat(length_out, "length_out", index, torch.int32, (self.B,))
-        if e.budget > 0:
-            self._workspace(e.budget)
+        if e.budget not in self._sized:
+            self._workspace(max(e.budget, 0))
+            self._sized.add(e.budget)
         _call("bsa_cache_evict", index, self._c, e, self._ws_ptr, self._ws_bytes)
         return scores_out, pos_out, length_out
 

@@ -121,7 +121,8 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
   __syncthreads();
   tc_fence_after();
   pdl_wait();
-  pdl_trigger();
+  // only the join may start under this kernel: another's kernel may not expect it
+  if (!WHOLE) pdl_trigger();
   const uint32_t tmem = *tmem_slot;
   Watchdog wd{abort_flag, p.cache.status, kWaitLimitNs};
   const RunStart run = *run_sm;

@@ -317,7 +317,6 @@ __global__ void __launch_bounds__(256) k_evict_move(const EvictArgs a, int per_h
   const int b = head / a.cache.H_kv, hk = head % a.cache.H_kv;
   const int sub = threadIdx.x % L, grp = threadIdx.x / L;
   pdl_wait();
-  pdl_trigger();
   // the block's moves of a step lie next to each other (rows of one DRAM page: 74 us with the groups' moves apart)
   const int m = a.count[head];
   const int64_t lb = static_cast<int64_t>(head) * a.list_cap, base = static_cast<int64_t>(head) * a.cache.capacity;

@@ -101,7 +101,6 @@ __global__ void __launch_bounds__(256, 4) k_rope(const RopeArgs a, const RopeGri
   const int rows = a.B * a.T, step = gridDim.x * g.tokens;  // rows < 2^31
 
   pdl_wait();
-  pdl_trigger();
   // the sines' side: this thread's pair, and every n_sub-th token of a step
   const int n_sub = pairs > 0 ? 256 / pairs : 0, p_sub = pairs > 0 ? threadIdx.x / pairs : 0;
   const int p_id = pairs > 0 ? threadIdx.x % pairs : 0;

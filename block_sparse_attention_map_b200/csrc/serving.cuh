@@ -74,6 +74,12 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 }
 
 // ---------------------------------------------------------------- launchers
+// Every kernel of these is launched with programmatic serialization and waits for
+// the stream's preceding kernel before it touches global memory, so its set-up
+// runs under that kernel's end.  Only k_attend and k_evict_select let their own
+// second kernel start early; no other kernel of the stream ever starts before one
+// of these is done.
+//
 // Raises a kernel's limit of dynamic shared memory, once per device and kernel
 // (`done` is the caller's own word, a bit a device).
 template <typename F>

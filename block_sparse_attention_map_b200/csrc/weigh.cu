@@ -89,7 +89,6 @@ __global__ void __launch_bounds__(128 + kSumThreads, 1) k_weigh(const __grid_con
   __syncthreads();
   tc_fence_after();
   pdl_wait();
-  pdl_trigger();
   const uint32_t tmem = *tmem_slot;
   Watchdog wd{abort_flag, p.cache.status, kWaitLimitNs};
   const RunStart run = *run_sm;
