@@ -25,7 +25,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kMaxSelCtas = 8;      // a portable cluster
+constexpr int kMaxSelCtas = 16;     // the largest cluster (above 8 a kernel has to ask for it)
 constexpr int kMaxKeys = 48 * 1024;  // of a CTA's slots in shared memory (more are read again for each pass)
 
 __device__ __forceinline__ uint32_t score_key(float s) {
@@ -69,9 +69,57 @@ __device__ __forceinline__ int2 count_warps(int2 (&warp_n)[kSelWarps + 1], int2 
   return warp_n[warp];
 }
 
+// The moves [0, m) of a head, by the part-th of `parts` blocks: a group of D/8
+// lanes moves one slot's K and V, the block's moves of a step next to each other
+// (rows of one DRAM page: 74 us against 50 for 16 heads of 65536 slots with the
+// groups' moves apart).
+__device__ __forceinline__ void move_rows(const EvictArgs &a, int head, int m, int part, int parts) {
+  constexpr int U = 2;  // moves of a group in flight
+  const int b = head / a.cache.H_kv, hk = head % a.cache.H_kv;
+  const int lanes = a.cache.D >> 3, moves = blockDim.x / lanes;
+  const int sub = threadIdx.x % lanes, grp = threadIdx.x / lanes;
+  const int64_t lb = static_cast<int64_t>(head) * a.list_cap, base = static_cast<int64_t>(head) * a.cache.capacity;
+  for (int i0 = part * U * moves + grp; i0 < m; i0 += parts * U * moves) {
+    int to[U], from[U], pt[U], pf[U];
+    int4 kv[U], vv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * moves;
+      to[u] = i < m ? a.to[lb + i] : -1;
+      from[u] = i < m ? a.from[lb + i] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      pt[u] = to[u] >= 0 ? page_of(a.cache, b, to[u]) : -1;
+      pf[u] = to[u] >= 0 ? page_of(a.cache, b, from[u]) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (pt[u] < 0 || pf[u] < 0) continue;
+      kv[u] = *reinterpret_cast<const int4 *>(a.cache.k + slot_offset(a.cache.ks, a.cache, pf[u], from[u], hk) + sub * 8);
+      vv[u] = *reinterpret_cast<const int4 *>(a.cache.v + slot_offset(a.cache.vs, a.cache, pf[u], from[u], hk) + sub * 8);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (to[u] < 0) continue;
+      if (pt[u] >= 0 && pf[u] >= 0) {
+        *reinterpret_cast<int4 *>(a.cache.k + slot_offset(a.cache.ks, a.cache, pt[u], to[u], hk) + sub * 8) = kv[u];
+        *reinterpret_cast<int4 *>(a.cache.v + slot_offset(a.cache.vs, a.cache, pt[u], to[u], hk) + sub * 8) = vv[u];
+      } else if (sub == 0) {
+        record_status(a.cache.status, BSA_ERR_BAD_CACHE);
+      }
+      if (sub == 0) {
+        a.score_out[base + to[u]] = a.mscore[lb + i0 + u * moves];
+        a.pos_out[base + to[u]] = a.mpos[lb + i0 + u * moves];
+      }
+    }
+  }
+}
+
 // K > 0: a thread's keys in K registers; K = 0: in shared memory where key_cap
-// holds them, else read again by each pass.
-template <int kSelThreads, int K>
+// holds them, else read again by each pass.  MOVES: the CTAs move their head's rows
+// too (and where the lengths do not change in place, write them).
+template <int kSelThreads, int K, bool MOVES>
 __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) k_evict_select(const EvictArgs a, int key_cap) {
   constexpr int kSelWarps = kSelThreads / 32;
   extern __shared__ uint32_t keys[];  // [key_cap]: this CTA's, where they fit
@@ -90,8 +138,10 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) k_evict_selec
   float *score_out = a.score_out + base;
   int32_t *pos_out = a.pos_out + base;
   pdl_trigger();
+  if (MOVES && a.length_out != a.cache.length && head % a.cache.H_kv == 0 && rank == 0 && tid == 0)
+    a.length_out[b] = min(n, a.budget);
   if (n <= a.budget) {  // the whole cluster
-    if (tid == 0 && rank == 0) a.count[head] = 0;
+    if (!MOVES && tid == 0 && rank == 0) a.count[head] = 0;
     if (score_out != score)
       for (int i = rank * kSelThreads + tid; i < n; i += ctas * kSelThreads) score_out[i] = score[i];
     if (pos_out != pos)
@@ -180,7 +230,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) k_evict_selec
       } else {
 #pragma unroll 1
         for (unsigned c0 = 0; c0 < ctas; c0 += 4) {
-          uint4 x[4], y[4];  // four CTAs' loads in flight (a cluster is 1, 4 or 8)
+          uint4 x[4], y[4];  // four CTAs' loads in flight (a cluster is 1, 4, 8 or 16)
 #pragma unroll
           for (unsigned c = 0; c < 4; ++c) {
             const uint4 *theirs = reinterpret_cast<const uint4 *>(cluster.map_shared_rank(mine, c0 + c) + 248 - 8 * lane);
@@ -254,17 +304,12 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) k_evict_selec
   int hole_at = in_cta.x, mover_at = in_cta.y, moved = counts[1][kSelWarps].y;
   if (ctas > 1) {
     cluster.sync();
-    moved = 0;
-    int2 t[kMaxSelCtas];
-#pragma unroll
-    for (unsigned c = 0; c < kMaxSelCtas; ++c)
-      t[c] = c < ctas ? cluster.map_shared_rank(&counts[1][kSelWarps], c)[0] : make_int2(0, 0);
-#pragma unroll
-    for (unsigned c = 0; c < kMaxSelCtas; ++c) {
-      hole_at += c < rank ? t[c].x : 0;
-      mover_at += c < rank ? t[c].y : 0;
-      moved += t[c].y;
-    }
+    // every lane one CTA's totals, added up over the warp
+    const int2 t = lane < static_cast<int>(ctas) ? cluster.map_shared_rank(&counts[1][kSelWarps], lane)[0] : make_int2(0, 0);
+    const bool lower = lane < static_cast<int>(rank);
+    hole_at += __reduce_add_sync(0xffffffffu, lower ? t.x : 0);
+    mover_at += __reduce_add_sync(0xffffffffu, lower ? t.y : 0);
+    moved = __reduce_add_sync(0xffffffffu, t.y);
   }
   int32_t *to = a.to + static_cast<int64_t>(head) * a.list_cap;
   int32_t *from = a.from + static_cast<int64_t>(head) * a.list_cap;
@@ -305,72 +350,43 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) k_evict_selec
     hole_at += __popc(hb);
     mover_at += __popc(mb);
   });
-  if (tid == 0 && rank == 0) a.count[head] = min(moved, a.list_cap);
-  if (ctas > 1) cluster.sync();  // no CTA leaves while another may read its shared memory
+  if (!MOVES && tid == 0 && rank == 0) a.count[head] = min(moved, a.list_cap);
+  // no CTA leaves while another may read its shared memory; and the lists are whole
+  if (ctas > 1) cluster.sync();
+  else __syncthreads();
+  if (MOVES) move_rows(a, head, min(moved, a.list_cap), rank, ctas);
 }
 
-template <int D>
+// The moves by every SM, and the new lengths (the selection is done with the old ones).
 __global__ void __launch_bounds__(256) k_evict_move(const EvictArgs a, int per_head) {
-  constexpr int L = D / 8;  // lanes a row
-  constexpr int kMoves = 256 / L, U = 2;  // moves of a block at a time, each group with U of them in flight
   const int head = blockIdx.x / per_head, part = blockIdx.x % per_head;
-  const int b = head / a.cache.H_kv, hk = head % a.cache.H_kv;
-  const int sub = threadIdx.x % L, grp = threadIdx.x / L;
   pdl_wait();
-  // the block's moves of a step lie next to each other (rows of one DRAM page: 74 us with the groups' moves apart)
-  const int m = a.count[head];
-  const int64_t lb = static_cast<int64_t>(head) * a.list_cap, base = static_cast<int64_t>(head) * a.cache.capacity;
-  for (int i0 = part * U * kMoves + grp; i0 < m; i0 += per_head * U * kMoves) {
-    int to[U], from[U], pt[U], pf[U];
-    int4 kv[U], vv[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kMoves;
-      to[u] = i < m ? a.to[lb + i] : -1;
-      from[u] = i < m ? a.from[lb + i] : -1;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      pt[u] = to[u] >= 0 ? page_of(a.cache, b, to[u]) : -1;
-      pf[u] = to[u] >= 0 ? page_of(a.cache, b, from[u]) : -1;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (pt[u] < 0 || pf[u] < 0) continue;
-      kv[u] = *reinterpret_cast<const int4 *>(a.cache.k + slot_offset(a.cache.ks, a.cache, pf[u], from[u], hk) + sub * 8);
-      vv[u] = *reinterpret_cast<const int4 *>(a.cache.v + slot_offset(a.cache.vs, a.cache, pf[u], from[u], hk) + sub * 8);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (to[u] < 0) continue;
-      if (pt[u] >= 0 && pf[u] >= 0) {
-        *reinterpret_cast<int4 *>(a.cache.k + slot_offset(a.cache.ks, a.cache, pt[u], to[u], hk) + sub * 8) = kv[u];
-        *reinterpret_cast<int4 *>(a.cache.v + slot_offset(a.cache.vs, a.cache, pt[u], to[u], hk) + sub * 8) = vv[u];
-      } else if (sub == 0) {
-        record_status(a.cache.status, BSA_ERR_BAD_CACHE);
-      }
-      if (sub == 0) {
-        a.score_out[base + to[u]] = a.mscore[lb + i0 + u * kMoves];
-        a.pos_out[base + to[u]] = a.mpos[lb + i0 + u * kMoves];
-      }
-    }
-  }
-  if (part == 0 && hk == 0 && threadIdx.x == 0) {
-    // k_evict_select is done with the lengths
-    const int n = min(max(a.cache.length[b], 0), a.cache.capacity);
-    a.length_out[b] = min(n, a.budget);
+  move_rows(a, head, a.count[head], part, per_head);
+  if (part == 0 && head % a.cache.H_kv == 0 && threadIdx.x == 0) {
+    const int b = head / a.cache.H_kv;
+    a.length_out[b] = min(min(max(a.cache.length[b], 0), a.cache.capacity), a.budget);
   }
 }
 
-template <int THREADS, int K>
+// The new lengths alone.
+__global__ void __launch_bounds__(256) k_evict_length(const EvictArgs a) {
+  const int b = blockIdx.x * 256 + threadIdx.x;
+  pdl_wait();
+  if (b < a.cache.B) a.length_out[b] = min(min(max(a.cache.length[b], 0), a.cache.capacity), a.budget);
+}
+
+template <int THREADS, int K, bool MOVES>
 cudaError_t select(const EvictArgs &a, int heads, int ctas, cudaStream_t s) {
   constexpr int kWarps = THREADS / 32;
+  const auto kernel = k_evict_select<THREADS, K, MOVES>;
   // a CTA's slots, at most
   const int share = ((a.cache.capacity + 31) / 32 + ctas * kWarps - 1) / (ctas * kWarps) * THREADS;
   const int key_cap = K == 0 && share <= kMaxKeys ? share : 0;
+  static std::atomic<uint64_t> smem_done{0}, size_done{0};
   cudaError_t e = cudaSuccess;
-  static std::atomic<uint64_t> done{0};
-  if (K == 0 && (e = allow_smem(k_evict_select<THREADS, K>, kMaxKeys * 4, done)) != cudaSuccess) return e;
+  if (K == 0 && (e = allow(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4, smem_done)) != cudaSuccess)
+    return e;
+  if (ctas > 8 && (e = allow(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1, size_done)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(heads) * ctas);
   cfg.blockDim = dim3(THREADS);
@@ -385,31 +401,46 @@ cudaError_t select(const EvictArgs &a, int heads, int ctas, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  count_launch(2);
-  return cudaLaunchKernelEx(&cfg, k_evict_select<THREADS, K>, a, key_cap);
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, a, key_cap);
+}
+
+template <int THREADS, int K>
+cudaError_t evict(const EvictArgs &a, int ctas, cudaStream_t s) {
+  const int heads = a.cache.B * a.cache.H_kv;
+  // The CTAs that select move the rows too where no more than a few can move (one
+  // launch less: 4097 slots to 4096 13.2 -> 11.6 us); else a second kernel on all SMs
+  // (32 heads of 32768 slots to half by the selecting CTAs: 107 us against 87).
+  if (a.list_cap <= 512) {
+    const cudaError_t e = select<THREADS, K, true>(a, heads, ctas, s);
+    if (e != cudaSuccess || a.length_out != a.cache.length) return e;
+    count_launch();
+    return launch_pdl(k_evict_length, dim3((a.cache.B + 255) / 256), dim3(256), 0, s, a);
+  }
+  const cudaError_t e = select<THREADS, K, false>(a, heads, ctas, s);
+  if (e != cudaSuccess) return e;
+  const int per_head = std::max(1, std::min((148 * 8 + heads - 1) / heads, (a.list_cap + 15) / 16));
+  count_launch();
+  return launch_pdl(k_evict_move, dim3(heads * per_head), dim3(256), 0, s, a, per_head);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s) {
-  const int heads = a.cache.B * a.cache.H_kv;
   // A head's slots are 8 a thread of one CTA up to 8192 (few slots in a large CTA
   // are slots for no one: 512 heads of 1025 slots 39 us with 1024 threads), else of
   // a cluster of CTAs of 512 threads, so that an SM holds two (16 clusters of 8 x
   // 1024 did not fit the GPU at once: 85 us against 37 for the selection of 65536).
   const int cap = a.cache.capacity;
-  cudaError_t e;
-  if (cap <= 2048) e = select<256, 8>(a, heads, 1, s);
-  else if (cap <= 4096) e = select<512, 8>(a, heads, 1, s);
-  else if (cap <= 8192) e = select<1024, 8>(a, heads, 1, s);
-  else if (cap <= 16384) e = select<512, 8>(a, heads, 4, s);
-  else if (cap <= 32768) e = select<512, 8>(a, heads, 8, s);
-  else e = select<512, 0>(a, heads, 8, s);  // (16 keys a thread spill: 43 us against 37 for 65536)
-  if (e != cudaSuccess) return e;
-  const int per_head = std::max(1, std::min((148 * 8 + heads - 1) / heads, (a.list_cap + 15) / 16));
-  return a.cache.D == 64
-             ? launch_pdl(k_evict_move<64>, dim3(heads * per_head), dim3(256), 0, s, a, per_head)
-             : launch_pdl(k_evict_move<128>, dim3(heads * per_head), dim3(256), 0, s, a, per_head);
+  if (cap <= 2048) return evict<256, 8>(a, 1, s);
+  if (cap <= 4096) return evict<512, 8>(a, 1, s);
+  if (cap <= 8192) return evict<1024, 8>(a, 1, s);
+  if (cap <= 16384) return evict<512, 8>(a, 4, s);
+  if (cap <= 32768) return evict<512, 8>(a, 8, s);
+  // 16 CTAs where the heads are few (1 head of 10^6 slots 836 -> 459 us; 16 heads of
+  // 65536 found too few places for such clusters: 94 -> 168 us)
+  if (a.cache.B * a.cache.H_kv <= 4) return cap <= 65536 ? evict<512, 8>(a, 16, s) : evict<512, 0>(a, 16, s);
+  return evict<512, 0>(a, 8, s);
 }
 
 }  // namespace bsa

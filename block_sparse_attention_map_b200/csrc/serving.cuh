@@ -80,18 +80,22 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 // second kernel start early; no other kernel of the stream ever starts before one
 // of these is done.
 //
-// Raises a kernel's limit of dynamic shared memory, once per device and kernel
-// (`done` is the caller's own word, a bit a device).
+// Sets an attribute of a kernel, once per device and kernel (`done` is the caller's
+// own word, a bit a device).
 template <typename F>
-cudaError_t allow_smem(F *kernel, int bytes, std::atomic<uint64_t> &done) {
+cudaError_t allow(F *kernel, cudaFuncAttribute what, int value, std::atomic<uint64_t> &done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
   if (bit != 0 && (done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  e = cudaFuncSetAttribute(kernel, what, value);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   return e;
+}
+template <typename F>
+cudaError_t allow_smem(F *kernel, int bytes, std::atomic<uint64_t> &done) {
+  return allow(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes, done);
 }
 
 struct RopeArgs {
