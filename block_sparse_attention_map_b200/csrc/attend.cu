@@ -461,8 +461,8 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
         f_mine *= inv;
         f_other *= inv;
         uint16_t *orow = p.out + w.b * p.os[0] + tok * p.os[1] + h * p.os[2];
-        // a piece that starts this CTA's run goes to slot 0, one that ends it to slot 1
-        const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (w.index > 0 ? 1 : 0)) * (kTile * NX) +
+        // a piece of the run's first item goes to slot 0, one of its last to slot 1
+        const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + w.slot) * (kTile * NX) +
                              (turns ? 0 : x * kTile) + r;
         float *prow = p.part_o + part * D;
         // the columns [c0, c1) * 16: half of them where both groups hold a part of the row
@@ -572,14 +572,24 @@ __global__ void __launch_bounds__(256) k_attend_join(const AttendParams p, int c
   uint16_t *orow = p.out + b * p.os[0] + t * p.os[1] + h * p.os[2] + lane * E;
   float *lse = p.lse + (static_cast<int64_t>(b) * p.tok.H + h) * p.tok.T + t;
   const bool padding = t >= s.n;
-  uint32_t c0 = 0, c1 = 0;
+  uint32_t c0 = 0, c1 = 0, units = 0;
+  int cost = 1;
   int64_t row_part = 0;
+  // whether run c has key tiles of this row's item
+  auto has = [&](uint32_t c) {
+    const uint32_t z = min(runs.start(c + 1) - a, units), y = runs.start(c) > a ? runs.start(c) - a : 0u;
+    return first_tile(y, cost) < first_tile(z, cost);
+  };
   if (in && !padding) {
-    // this row's item in the list: [a, a + tiles)
+    // this row's item in the list: [a, a + units)
     const int hk = h / p.tok.G, row = t * p.tok.G + h % p.tok.G, rg = row / (kTile * NX);
-    a += (static_cast<uint32_t>(hk) * s.groups + rg) * s.tiles;
+    a += static_cast<uint32_t>(hk) * s.head_units() + s.group_start(rg);
+    units = s.units(rg);
+    cost = s.cost(rg);
     c0 = runs.of(a);
-    c1 = runs.of(a + s.tiles - 1);
+    c1 = runs.of(a + units - 1);
+    if (NX == 2)
+      while (c1 > c0 && !has(c1)) --c1;
     row_part = row - rg * kTile * NX;
   }
   const bool joined = c0 != c1;  // else one run has written the row
@@ -590,18 +600,20 @@ __global__ void __launch_bounds__(256) k_attend_join(const AttendParams p, int c
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   if (joined) {
-    // the runs c0 .. c1 are not empty; c0's piece is its last, unless it starts there
+    // c0's piece is its run's last, unless the run starts there
     auto part_of = [&](uint32_t c) {
       const int slot = runs.start(c) >= a ? 0 : 1;
       return (static_cast<int64_t>(c) * 2 + slot) * (kTile * NX) + row_part;
     };
-    for (uint32_t c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_ml[part_of(c)].x);
+    for (uint32_t c = c0 + lane; c <= c1; c += 32)
+      if (NX == 1 || has(c)) M = fmaxf(M, p.part_ml[part_of(c)].x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
     const float Mu = M == -INFINITY ? 0.f : M;
     const uint32_t n = c1 - c0 + 1, z = c0 + n * (sub + 1) / WARPS;
 #pragma unroll 4
     for (uint32_t c = c0 + n * sub / WARPS; c < z; ++c) {
+      if (NX == 2 && !has(c)) continue;
       const int64_t part = part_of(c);
       const float4 ml = p.part_ml[part];
       const float f = exp2f(ml.x - Mu);

@@ -9,16 +9,32 @@ namespace bsa {
 
 // Sequence b has H_kv * groups(b) items of tiles(b) key tiles each, a row group
 // being ROWS of its n * G rows (kAllRows: one group, even of no row); the list is
-// all of them in order (b, kv head, row group, tile).
-// With WHOLE, the list is of items instead, every row of the T * G in one, and a
-// run takes each item from its first tile to its last.
+// all of them in order (b, kv head, row group, tile).  It is measured in units: a
+// key tile of a group with two row tiles is 3, of one with a single one 2 (4240
+// against about 2700 clocks measured; with equal shares of tiles 2 sequences x 64
+// tokens x 5 heads a group, rows 256 + 64, over 75600 keys took 341 us, now 306),
+// where every group is alike 1.  With WHOLE, the list is of items instead, every
+// row of the T * G in one, and a run takes each from its first tile to its last.
 constexpr int kAllRows = 0;
 
 template <int ROWS, bool WHOLE = false>
 struct Seq {
   int len, n, tiles, groups;
-  __device__ __forceinline__ uint32_t units() const { return WHOLE ? 1u : tiles; }  // of an item
-  __device__ __forceinline__ uint32_t work(int H_kv) const { return static_cast<uint32_t>(H_kv) * groups * units(); }
+  int last;  // the cost of a tile of the last group
+  static constexpr int kCost = ROWS > kTile && !WHOLE ? 3 : 1;  // of the others
+  __device__ __forceinline__ int cost(int rg) const { return kCost == 1 ? 1 : rg == groups - 1 ? last : kCost; }
+  // units of an item, and of a kv head
+  __device__ __forceinline__ uint32_t units(int rg) const { return WHOLE ? 1u : static_cast<uint32_t>(tiles) * cost(rg); }
+  __device__ __forceinline__ uint32_t head_units() const {
+    if (WHOLE) return groups;
+    if (kCost == 1) return static_cast<uint32_t>(tiles) * groups;
+    return groups == 0 ? 0u : static_cast<uint32_t>(tiles) * ((groups - 1) * kCost + last);
+  }
+  __device__ __forceinline__ uint32_t work(int H_kv) const { return H_kv * head_units(); }
+  // the first unit of group rg within its kv head
+  __device__ __forceinline__ uint32_t group_start(int rg) const {
+    return WHOLE ? rg : static_cast<uint32_t>(tiles) * kCost * rg;
+  }
 };
 
 template <int ROWS, bool WHOLE = false>
@@ -28,11 +44,12 @@ __device__ __forceinline__ Seq<ROWS, WHOLE> sequence(const CacheView &c, const T
   s.n = clamped_new(c, t, b, s.len, report);
   s.tiles = WHOLE && s.n == 0 ? 0 : (s.len + s.n + kTile - 1) / kTile;
   s.groups = ROWS == kAllRows ? min(s.tiles, 1) : ((WHOLE ? t.T : s.n) * t.G + max(ROWS, 1) - 1) / max(ROWS, 1);
+  s.last = s.kCost == 1 ? 1 : s.n * t.G - (s.groups - 1) * ROWS > kTile ? 3 : 2;
   return s;
 }
 
-// The list (fewer than 2^31 tiles) in `ctas` runs of one length, the first ones a
-// tile longer: run c is [start(c), start(c + 1)).
+// The list (fewer than 2^31 units) in `ctas` runs of one length, the first ones a
+// unit longer: run c is [start(c), start(c + 1)).
 struct Runs {
   uint32_t total, base, rem;
   __device__ __forceinline__ Runs(uint32_t total_, int ctas)
@@ -46,7 +63,7 @@ struct Runs {
 };
 
 struct RunStart {
-  int b, item, tile, count;  // count: key tiles of the run
+  int b, item, at, count;  // at: units into the item; count: units of the run
 };
 
 // Length of the list, and of its part before sequence `upto`, by one warp.
@@ -70,7 +87,7 @@ __device__ __forceinline__ RunStart find_start(const CacheView &c, const TokenVi
   RunStart r{0, 0, 0, count};
   uint32_t base = 0;
   for (int b0 = 0; b0 < c.B; b0 += 32) {
-    Seq<ROWS, WHOLE> s{0, 0, 0, 0};
+    Seq<ROWS, WHOLE> s{0, 0, 0, 0, 1};
     if (b0 + lane < c.B) s = sequence<ROWS, WHOLE>(c, t, b0 + lane, false);
     const uint32_t w = s.work(c.H_kv);
     uint32_t incl = w;
@@ -84,10 +101,17 @@ __device__ __forceinline__ RunStart find_start(const CacheView &c, const TokenVi
     const uint32_t who = __ballot_sync(0xffffffffu, here);
     if (who != 0u) {
       const int src = __ffs(who) - 1;
-      const int item = here ? static_cast<int>(off / s.units()) : 0, tile = here ? static_cast<int>(off % s.units()) : 0;
+      int item = 0, into = 0;
+      if (here) {
+        const uint32_t hk = off / s.head_units(), rest = off - hk * s.head_units();
+        const uint32_t other = WHOLE ? 1u : static_cast<uint32_t>(s.tiles) * s.kCost;
+        const int rg = min(static_cast<int>(rest / other), s.groups - 1);
+        item = static_cast<int>(hk) * s.groups + rg;
+        into = static_cast<int>(rest - s.group_start(rg));
+      }
       r.b = b0 + src;
       r.item = __shfl_sync(0xffffffffu, item, src);
-      r.tile = __shfl_sync(0xffffffffu, tile, src);
+      r.at = __shfl_sync(0xffffffffu, into, src);
       return r;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
@@ -105,34 +129,44 @@ __device__ __forceinline__ RunStart find_run(const CacheView &c, const TokenView
   return z > a ? find_start<ROWS, WHOLE>(c, t, a, static_cast<int>(z - a), lane) : RunStart{0, 0, 0, 0};
 }
 
+// The key tiles of the units [p0, p1) of an item: those that begin in them.
+__device__ __forceinline__ int first_tile(uint32_t p, int cost) { return static_cast<int>((p + cost - 1) / cost); }
+
 // One CTA's run, piece by piece (a piece: consecutive key tiles of one item).
 template <int ROWS, bool WHOLE = false>
 struct Walk {
-  int b, item, tile, left, index;
+  int b, item, at, left, index, slot;
   Seq<ROWS, WHOLE> s;
   int hk, rg, t0, t1;  // the piece: kv head, row group, key tiles [t0, t1)
   bool whole;
   __device__ __forceinline__ Walk(const CacheView &c, const TokenView &t, const RunStart &r)
-      : b(r.b), item(r.item), tile(r.tile), left(r.count), index(-1) {
+      : b(r.b), item(r.item), at(r.at), left(r.count), index(-1), slot(-1) {
     if (left > 0) s = sequence<ROWS, WHOLE>(c, t, b, false);
   }
+  // index counts the pieces; slot is 0 in the run's first item, else 1
   __device__ __forceinline__ bool next(const CacheView &c, const TokenView &t) {
-    if (left <= 0) return false;
-    while (item >= c.H_kv * s.groups) {
-      item = 0;
-      if (++b >= c.B) return false;  // never, with lengths that stay as they are
-      s = sequence<ROWS, WHOLE>(c, t, b, false);
+    while (left > 0) {
+      while (item >= c.H_kv * s.groups) {
+        item = 0;
+        if (++b >= c.B) return false;  // never, with lengths that stay as they are
+        s = sequence<ROWS, WHOLE>(c, t, b, false);
+      }
+      hk = item / s.groups;
+      rg = item % s.groups;
+      const int units = static_cast<int>(s.units(rg)), end = min(units, at + left);
+      t0 = WHOLE ? 0 : first_tile(at, s.cost(rg));
+      t1 = WHOLE ? s.tiles : first_tile(end, s.cost(rg));
+      whole = t0 == 0 && t1 == s.tiles;
+      left -= end - at;
+      at = 0;
+      ++item;
+      slot = min(slot + 1, 1);
+      if (WHOLE || t0 < t1) {
+        ++index;
+        return true;
+      }
     }
-    hk = item / s.groups;
-    rg = item % s.groups;
-    t0 = tile;
-    t1 = WHOLE ? s.tiles : min(s.tiles, tile + left);
-    whole = t0 == 0 && t1 == s.tiles;
-    left -= WHOLE ? 1 : t1 - t0;
-    tile = 0;
-    ++item;
-    ++index;
-    return true;
+    return false;
   }
 };
 

@@ -188,9 +188,9 @@ bsa_status check_reading(const bsa_cache *cache, const bsa_tokens *tok, CacheVie
   if ((st = check_tokens(tok, false, t)) != BSA_OK) return st;
   if (!matches(*cache, t->t) || t->t.T > kMaxTree) return BSA_ERR_INVALID_ARG;
   if (t->t.H / t->t.H_kv > kMaxGroup) return BSA_ERR_UNSUPPORTED;
-  // key tiles of all heads and row groups: 31 bits
+  // units of work of all heads and row groups (up to 3 a tile): 31 bits
   const int64_t rows = static_cast<int64_t>(t->t.T) * (t->t.H / t->t.H_kv);
-  if (static_cast<int64_t>(c->B) * c->H_kv * (c->capacity / kTile + 1) >= (int64_t{1} << 31) / (rows / kTile + 1))
+  if (static_cast<int64_t>(c->B) * c->H_kv * (c->capacity / kTile + 1) >= (int64_t{1} << 29) / (rows / kTile + 1))
     return BSA_ERR_UNSUPPORTED;
   if (!aligned4(t->t.n_new) || (reinterpret_cast<uintptr_t>(t->t.tree) & 7u)) return BSA_ERR_UNSUPPORTED;
   return BSA_OK;

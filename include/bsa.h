@@ -573,7 +573,7 @@ BSA_API bsa_status bsa_cache_append(const bsa_cache *cache, const bsa_tokens *to
  * K and V of what a row does not see never reach it, NaN and infinities
  * included.  The same inputs give the same bits.
  * Errors as for bsa_cache_append; INVALID_ARG also for T > 64, UNSUPPORTED for
- * H / H_kv > 128 and for 2^31 or more tiles of 128 slots over all sequences, key
+ * H / H_kv > 128 and for 2^29 or more tiles of 128 slots over all sequences, key
  * heads and groups of 128 rows. */
 BSA_API bsa_status bsa_cache_attend(const bsa_cache *cache, const bsa_tokens *tok, const void *q, void *out,
                                     float *lse, void *ws, size_t ws_bytes, bsa_stream_t stream);
