@@ -19,6 +19,7 @@ from ._binding import (  # noqa: F401
     workspace_size,
 )
 from ._serving import (  # noqa: F401
+    CacheWorkspace,
     PagedCache,
     rope,
     rope_bwd,

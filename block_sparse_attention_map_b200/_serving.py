@@ -286,6 +286,29 @@ def _append_layout(ks, kt, vs, vt, qs, qt, qos, qot, ps, pt, fs, axs, layout, B,
     return t, r, q and q[2:]
 
 
+class CacheWorkspace:
+    """Scratch memory and the sticky status word of paged caches' calls.  Caches
+    whose calls all follow one another on one stream (the layers of a model) may
+    share one; it grows to what the largest call needs."""
+
+    def __init__(self, device):
+        self.device = torch.device(device)
+        self.buf, self.ptr, self.nbytes = None, None, 0
+
+    def grow(self, nbytes):
+        """At least ``nbytes``, the status word kept."""
+        if nbytes <= self.nbytes:
+            return
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the workspace cannot grow while a stream is captured: reserve() before the capture")
+        new = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        if self.buf is None:
+            new[:256].zero_()
+        else:
+            new[:256].copy_(self.buf[:256])
+        self.buf, self.ptr, self.nbytes = new, new.data_ptr(), nbytes
+
+
 class PagedCache:
     """A paged key/value cache and the calls around it.
 
@@ -296,11 +319,12 @@ class PagedCache:
     ``length`` in place as tokens are accepted.  Only :meth:`append` and
     :meth:`evict` write the cache, in place.
 
-    The calls of one PagedCache share a workspace, so they belong on one stream
-    at a time; use one PagedCache (over the same tensors) per concurrent stream
-    or captured graph."""
+    The calls of one PagedCache share a workspace (its own, or the ``workspace``
+    given), so they belong on one stream at a time; use a PagedCache (over the
+    same tensors) and workspace for each stream, and for each captured graph that
+    may run beside another.  :meth:`reserve` before a capture that evicts."""
 
-    def __init__(self, k, v, page_table, length):
+    def __init__(self, k, v, page_table, length, workspace: Optional[CacheWorkspace] = None):
         if not k.is_cuda or k.dim() != 4 or k.dtype not in DTYPE:
             raise ValueError("k and v are [n_pages, page_size, H_kv, D] bf16 or fp16 CUDA tensors")
         if v.shape != k.shape:
@@ -321,20 +345,18 @@ class PagedCache:
         c.page_table = page_table.data_ptr()
         c.table_stride = page_table.stride(0) if self.B > 1 else 0
         c.length = _flat(length, "length", self._index, torch.int32, (self.B,))
-        self._ws, self._sized = None, set()  # budgets the workspace holds
-        self._workspace(0)
+        self.workspace = CacheWorkspace(self.device) if workspace is None else workspace
+        if self.workspace.device != self.device:
+            raise ValueError("workspace: on another device")
+        self._reserved = set()  # budgets the workspace holds
+        self.reserve(0)
 
-    def _workspace(self, budget):
-        """The workspace, grown to what an eviction to ``budget`` needs (the status word is kept)."""
+    def reserve(self, budget):
+        """Grows the workspace to what evictions to ``budget`` need."""
         n = ctypes.c_size_t(0)
         _check(_fn("bsa_cache_workspace_size")(self._c, budget, ctypes.byref(n)), "bsa_cache_workspace_size")
-        if self._ws is None or self._ws_bytes < n.value:
-            new = torch.empty(n.value, dtype=torch.uint8, device=self.device)
-            if self._ws is None:
-                new[:256].zero_()
-            else:
-                new[:256].copy_(self._ws[:256])
-            self._ws, self._ws_ptr, self._ws_bytes = new, new.data_ptr(), n.value
+        self.workspace.grow(n.value)
+        self._reserved.add(budget)
 
     def _token_layout(self, shape, stride, out_shape, out_stride, scale):
         if len(shape) != 4 or shape[3] != self.D:
@@ -394,7 +416,7 @@ class PagedCache:
             _check_apart(qp, qop, *qa, "q_out")
         if rp is not None:
             r = _rope_args(rp, pos, inv_freq, axis)
-        _call("bsa_cache_append", index, self._c, t, r, qp, qop, k.data_ptr(), v.data_ptr(), self._ws_ptr, self._ws_bytes)
+        _call("bsa_cache_append", index, self._c, t, r, qp, qop, k.data_ptr(), v.data_ptr(), self.workspace.ptr, self.workspace.nbytes)
         return q_out
 
     def attend(self, q, tree=None, n_new=None, scale=None, out=None, lse=None):
@@ -412,7 +434,7 @@ class PagedCache:
         if lse is None:
             lse = torch.empty(B, H, T, dtype=torch.float32, device=self.device)
         _call("bsa_cache_attend", self._index, self._c, t, q.data_ptr(), out.data_ptr(),
-              _flat(lse, "lse", self._index, torch.float32, (B, H, T)), self._ws_ptr, self._ws_bytes)
+              _flat(lse, "lse", self._index, torch.float32, (B, H, T)), self.workspace.ptr, self.workspace.nbytes)
         return out, lse
 
     def weigh(self, q, lse, scores, tree=None, n_new=None, scale=None, out=None):
@@ -426,7 +448,7 @@ class PagedCache:
         score_in = _flat(scores, "scores", self._index, torch.float32, shape)
         score_out = score_in if out is None else _flat(out, "out", self._index, torch.float32, shape)
         _call("bsa_cache_weigh", self._index, self._c, t, q.data_ptr(),
-              _flat(lse, "lse", self._index, torch.float32, (B, H, T)), score_in, score_out, self._ws_ptr, self._ws_bytes)
+              _flat(lse, "lse", self._index, torch.float32, (B, H, T)), score_in, score_out, self.workspace.ptr, self.workspace.nbytes)
         return scores if out is None else out
 
     def evict(self, scores, pos, next_pos, budget, sinks=0, recent=0, scores_out=None, pos_out=None,
@@ -450,13 +472,12 @@ class PagedCache:
         e.score_out = e.score_in if scores_out is scores else _flat(scores_out, "scores_out", index, torch.float32, shape)
         e.pos_out = e.pos_in if pos_out is pos else _flat(pos_out, "pos_out", index, torch.int32, shape)
         e.length_out = _flat(length_out, "length_out", index, torch.int32, (self.B,))
-        if e.budget not in self._sized:
-            self._workspace(max(e.budget, 0))
-            self._sized.add(e.budget)
-        _call("bsa_cache_evict", index, self._c, e, self._ws_ptr, self._ws_bytes)
+        if e.budget not in self._reserved:
+            self.reserve(max(e.budget, 0))
+        _call("bsa_cache_evict", index, self._c, e, self.workspace.ptr, self.workspace.nbytes)
         return scores_out, pos_out, length_out
 
     def status(self, clear=False):
         """The sticky device status of this cache's calls (0: ok; synchronises)."""
         with torch.cuda.device(self._index):
-            return int(lib().bsa_get_device_status(self._ws_ptr, self._ws_bytes, _stream_of(self._index), 1 if clear else 0))
+            return int(lib().bsa_get_device_status(self.workspace.ptr, self.workspace.nbytes, _stream_of(self._index), 1 if clear else 0))

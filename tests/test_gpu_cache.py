@@ -48,6 +48,8 @@ ATTEND = [  # lengths, T, H, H_kv, D, page, dtype, n_new, tree
     ([2500, 17, 900], 3, 40, 8, 128, 64, "bf16", [3, 3, 2], "random"),
     ([130, 2], 2, 128, 1, 64, 32, "bf16", None, "random"),
     ([600], 5, 100, 1, 128, 32, "fp16", None, "random"),
+    ([20000], 2, 4, 1, 64, 64, "bf16", None, "random"),   # a run a tile or two: every SM has a piece of the same rows
+    ([6000, 1], 40, 8, 1, 64, 128, "bf16", [40, 3], "random"),  # two row tiles and one, many pieces
 ]
 
 
@@ -120,6 +122,55 @@ def test_what_a_row_does_not_see_never_reaches_it(T, G):
                         assert torch.isnan(got).all() if math.isnan(bad) else torch.equal(got, torch.full_like(got, bad))
                     else:
                         assert torch.equal(out[b, t], ref_out[b, t])
+
+
+@pytest.mark.parametrize("T", [1, 5])
+def test_many_sequences_of_any_length(T):
+    """More sequences than a warp scans at once, most of them short or empty."""
+    rng = np.random.default_rng(T)
+    lengths = [int(rng.integers(0, 900)) if rng.random() < 0.3 else int(rng.integers(0, 3)) for _ in range(77)]
+    new = [int(rng.integers(0, T + 1)) for _ in range(77)]
+    st = Setup(lengths, T, 2, 1, 64, 16, seed=50 + T, n_new=new)
+    cache = st.cache()
+    out, lse = cache.attend(st.q, st.tree, st.n_new)
+    L = check_attend(st, out, lse)
+    scores = torch.zeros(77, 1, cache.capacity, device="cuda")
+    cache.weigh(st.q, torch.from_numpy(L).float().cuda(), scores, st.tree, st.n_new)
+    assert cache.status() == 0
+    seen = np.isfinite(L).sum((1, 2))  # every row that sees something spreads a weight of 1
+    assert np.allclose(scores.sum((1, 2)).cpu().numpy(), seen, rtol=1e-4, atol=1e-5)
+
+
+def test_a_cache_past_32_bits():
+    """Element offsets of K and V past 2^32: a few pages at the far end of a large cache."""
+    st = Setup([700, 90], 3, 4, 2, 128, 64, seed=60, spare=30)
+    n = (1 << 32) // (64 * 2 * 128) + 40
+    k = torch.empty(n, 64, 2, 128, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    used = st.k.shape[0]
+    k[n - used:], v[n - used:] = st.k, st.v
+    far = bsa.PagedCache(k, v, st.table + (n - used), st.length)
+    near = st.cache()
+    out, lse = far.attend(st.q, st.tree)
+    want = near.attend(st.q, st.tree)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    sc = torch.rand(2, 2, near.capacity, generator=st.g, device="cuda")
+    pos = torch.arange(near.capacity, dtype=torch.int32, device="cuda").expand(2, 2, -1).contiguous()
+    far_sc, far_pos = sc.clone(), pos.clone()
+    for c, s, p in ((near, sc, pos), (far, far_sc, far_pos)):
+        c.weigh(st.q, lse, s, st.tree)
+    assert torch.equal(sc, far_sc)
+    nk, nv = normal(st.g, (2, 3, 2, 128), "bf16"), normal(st.g, (2, 3, 2, 128), "bf16")
+    nxt = torch.tensor([5000, 5000], dtype=torch.int32, device="cuda")
+    far.append(nk, nv)
+    near.append(nk, nv)
+    far_len = st.length.clone()
+    near.evict(sc, pos, nxt, 300, length_out=torch.empty_like(far_len))
+    far.evict(far_sc, far_pos, nxt, 300, length_out=far_len)
+    assert torch.equal(sc, far_sc) and torch.equal(pos, far_pos) and far_len.tolist() == [300, 90]
+    assert torch.equal(k[n - used:].view(torch.int16), st.k.view(torch.int16))
+    assert torch.equal(v[n - used:].view(torch.int16), st.v.view(torch.int16))
+    assert far.status() == 0
 
 
 def test_words_that_leave_rows_empty_and_bits_past_the_new_tokens():
@@ -262,6 +313,52 @@ def test_evict_matches_oracle(lengths, H_kv, page, dtype, D, budget, sinks, rece
     cache.evict(score, pos, next_pos, budget, sinks, recent)
     check_evict(st, (k0, v0), s0, p0, next_pos.tolist(), budget, sinks, recent, score.cpu().numpy(), pos.cpu().numpy(),
                 st.length.tolist(), (s0, p0))
+
+
+@pytest.mark.parametrize("keys,H_kv,D,budget", [
+    (2000, 3, 64, 1700), (4000, 2, 64, 3999), (8000, 2, 128, 100), (12000, 2, 64, 6000), (30000, 2, 64, 17001),
+    (50000, 5, 64, 20000), (50000, 3, 64, 49990), (150000, 1, 64, 70000), (900000, 1, 64, 400000)])
+def test_evict_of_every_size(keys, H_kv, D, budget):
+    """One call of each way the selection is laid out (slots a CTA, cluster sizes, keys
+    in registers, in shared memory and read again), against a stable sort."""
+    g = gen(keys)
+    page, B = 64, 2 if keys < 100000 else 1
+    per = -(-keys // page)
+    n_pages = B * per
+    k = torch.randn(n_pages, page, H_kv, D, generator=g, device="cuda", dtype=torch.bfloat16)
+    v = torch.randn(n_pages, page, H_kv, D, generator=g, device="cuda", dtype=torch.bfloat16)
+    table = torch.randperm(n_pages, generator=g, device="cuda").view(B, per).int()
+    lengths = [keys - 7, keys - keys // 3][:B]
+    length = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    cache = bsa.PagedCache(k, v, table, length)
+    score = (torch.randn(B, H_kv, cache.capacity, generator=g, device="cuda") * 50).round()  # many equal ones
+    pos = torch.stack([torch.randperm(cache.capacity, generator=g, device="cuda") for _ in range(B * H_kv)]).int()
+    pos = pos.view(B, H_kv, -1).contiguous()
+    nxt = torch.full((B,), cache.capacity, dtype=torch.int32, device="cuda")
+    k0, v0, s0, p0 = k.clone(), v.clone(), score.clone(), pos.clone()
+    cache.evict(score, pos, nxt, budget, sinks=5, recent=budget // 3)
+    assert cache.status() == 0 and length.tolist() == [min(n, budget) for n in lengths]
+    slot = torch.arange(cache.capacity, device="cuda")
+    for b in range(B):
+        n, page_of = lengths[b], table[b].long()
+        for h in range(H_kv):
+            src = slot[:min(n, budget)].clone()
+            if n > budget:
+                p, s = p0[b, h, :n], s0[b, h, :n]
+                must = (p < 5) | (p >= int(nxt[b]) - budget // 3)
+                rank = torch.where(must, math.inf, s)
+                keep = torch.sort(rank, descending=True, stable=True).indices[:budget]
+                kept = torch.zeros(n, dtype=torch.bool, device="cuda")
+                kept[keep] = True
+                src[~kept[:budget]] = slot[budget:n][kept[budget:]]
+            to, fr = slot[:src.numel()], src
+            assert torch.equal(score[b, h, to], s0[b, h, fr]) and torch.equal(pos[b, h, to], p0[b, h, fr])
+            assert (score[b, h, src.numel():n] == 0).all() and (pos[b, h, src.numel():n] == -1).all()
+            assert torch.equal(score[b, h, n:], s0[b, h, n:])
+            for x, x0 in ((k, k0), (v, v0)):
+                assert torch.equal(x[page_of[to // page], to % page, h], x0[page_of[fr // page], fr % page, h])
+                late = slot[src.numel():n]
+                assert torch.equal(x[page_of[late // page], late % page, h], x0[page_of[late // page], late % page, h])
 
 
 def test_evict_orders_odd_scores():
@@ -412,8 +509,8 @@ def test_a_captured_step_replays_on_another_stream():
     io = inputs(0)
     warm = make()
     step(*warm, io)  # everything the capture needs is there (the workspace's size among it)
-    a[1].evict(a[2], a[3], a[4], 10000)  # grows a's workspace, moves nothing
-    a[1]._workspace(150)
+    torch.cuda.synchronize()
+    a[1].reserve(150)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
@@ -435,6 +532,31 @@ def test_a_captured_step_replays_on_another_stream():
         assert torch.equal(a[0].k, b[0].k) and torch.equal(a[0].v, b[0].v)
         assert a[1].length.tolist() == b[1].length.tolist() == [150, 150]
     assert a[1].status() == 0 and b[1].status() == 0
+
+
+def test_caches_may_share_a_workspace():
+    st = Setup([300, 40], 2, 4, 2, 64, 16, seed=70)
+    ws = bsa.CacheWorkspace("cuda:0")
+    a, b = (bsa.PagedCache(st.k, st.v, st.table, st.length, workspace=ws) for _ in range(2))
+    want = st.cache().attend(st.q, st.tree)
+    for c in (a, b, a):
+        got = c.attend(st.q, st.tree)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    st.table[0, 0] = -1
+    b.attend(st.q, st.tree)
+    assert a.status(clear=True) == 11 and b.status() == 0
+    with pytest.raises(ValueError):
+        bsa.PagedCache(st.k, st.v, st.table, st.length, workspace=bsa.CacheWorkspace("cpu"))
+    torch.cuda.synchronize()
+    before = ws.nbytes
+    with pytest.raises(RuntimeError):  # a capture must not hold the memory of later eager calls
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            torch.zeros(1, device="cuda")
+            ws.grow(2 * before)
+    assert ws.nbytes == before
+    ws.grow(2 * before)
+    got = a.attend(st.q, st.tree)
+    assert b.status(clear=True) == 11 and got[0].shape == st.q.shape
 
 
 def test_refusals():

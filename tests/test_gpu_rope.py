@@ -39,6 +39,8 @@ CASES = [  # B, S, H, H_kv, D, n_axes, n_pairs, layout, dtype
     (1, 65, 2, 2, 256, 8, 128, "halves", "bf16"),
     (1, 9, 2, 1, 80, 2, 40, "interleaved", "bf16"),
     (1, 5, 3, 3, 16, 1, 8, "halves", "fp16"),
+    (1, 40000, 1, 1, 128, 3, 64, "interleaved", "bf16"),  # more tokens than one step of the grid
+    (2, 3000, 45, 3, 64, 2, 32, "halves", "bf16"),
 ]
 
 
@@ -162,6 +164,18 @@ def test_append_writes_its_slots_and_nothing_else(layout, dtype, D, page):
     if layout:
         assert torch.equal(q, bsa.rope(st.q, None, pos, freq, axis, layout)[0])
     assert cache.status() == 0 and st.length.tolist() == st.lengths
+
+
+def test_append_of_a_long_prompt():
+    st = Setup([3, 40], 300, 2, 2, 64, 32, seed=7, n_new=[300, 211], spare=10, tree=None)
+    k, v = normal(st.g, (2, 300, 2, 64), "bf16"), normal(st.g, (2, 300, 2, 64), "bf16")
+    cache = st.cache()
+    cache.append(k, v, n_new=st.n_new)
+    assert cache.status() == 0
+    for b in range(2):
+        s = np.arange(st.lengths[b], st.lengths[b] + st.new[b])
+        at = torch.from_numpy(st.table_np[b][s // 32].astype(np.int64)).cuda(), torch.from_numpy(s % 32).cuda()
+        assert torch.equal(st.k[at], k[b, :st.new[b]]) and torch.equal(st.v[at], v[b, :st.new[b]])
 
 
 def test_append_past_the_capacity_or_a_bad_page_writes_nothing_there():
