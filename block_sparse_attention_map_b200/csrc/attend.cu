@@ -319,36 +319,39 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
             else if (d0 >= 0) allow[q] = static_cast<uint32_t>(word >> d0);
             else if (d0 > -32) allow[q] = static_cast<uint32_t>(word << -d0) | ((1u << -d0) - 1u);
           }
-          if (turns || x == 0) {
-            // this thread's key: V past the new tokens becomes zero, what is not
-            // finite in a new token's V is taken out
-            if (!wwait(&bars[L::bVFull + kv % NV], (kv / NV) & 1)) { stop = true; break; }
-            uint8_t *vrow = sm + L::kV + (kv % NV) * kTB + r * 128;
-            const int d = j0 + r - w.s.len;
-            if (d >= 0) {
-              bool found = false;
-#pragma unroll 8
-              for (int c = 0; c < kPieces; ++c) {
-                int4 *q4 = reinterpret_cast<int4 *>(vrow + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4));
-                int4 v = make_int4(0, 0, 0, 0);
-                if (d < w.s.n) {
-                  v = *q4;
-                  const uint32_t n0 = not_finite<FP16>(v.x), n1 = not_finite<FP16>(v.y), n2 = not_finite<FP16>(v.z),
-                                 n3 = not_finite<FP16>(v.w);
-                  if ((n0 | n1 | n2 | n3) == 0u) continue;
-                  found = true;
-                  v = make_int4(v.x & ~n0, v.y & ~n1, v.z & ~n2, v.w & ~n3);
-                }
-                *q4 = v;
-              }
-              if (found) atomicOr(bad_w + (d >> 5), 1u << (d & 31));
-              fence_proxy_async_smem();
-            }
-            __syncwarp();
-          }
         }
         if (!wwait(&bars[L::bSFull + x], used & 1)) { stop = true; break; }
         tc_fence_after();
+        // After S: the products of the tiles that had this V stage before are done (they were issued before S), so
+        // the stage's phase is this tile's.  (Waited for before S, it could still be at the tile before in the stage,
+        // whose V this would have zeroed.)
+        if (edge && (turns || x == 0)) {
+          // this thread's key: V past the new tokens becomes zero, what is not
+          // finite in a new token's V is taken out
+          if (!wwait(&bars[L::bVFull + kv % NV], (kv / NV) & 1)) { stop = true; break; }
+          uint8_t *vrow = sm + L::kV + (kv % NV) * kTB + r * 128;
+          const int d = j0 + r - w.s.len;
+          if (d >= 0) {
+            bool found = false;
+#pragma unroll 8
+            for (int c = 0; c < kPieces; ++c) {
+              int4 *q4 = reinterpret_cast<int4 *>(vrow + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4));
+              int4 v = make_int4(0, 0, 0, 0);
+              if (d < w.s.n) {
+                v = *q4;
+                const uint32_t n0 = not_finite<FP16>(v.x), n1 = not_finite<FP16>(v.y), n2 = not_finite<FP16>(v.z),
+                               n3 = not_finite<FP16>(v.w);
+                if ((n0 | n1 | n2 | n3) == 0u) continue;
+                found = true;
+                v = make_int4(v.x & ~n0, v.y & ~n1, v.z & ~n2, v.w & ~n3);
+              }
+              *q4 = v;
+            }
+            if (found) atomicOr(bad_w + (d >> 5), 1u << (d & 31));
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+        }
         if (warp_on) {
           uint32_t sv[4][32];
 #pragma unroll

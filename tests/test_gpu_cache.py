@@ -141,6 +141,55 @@ def test_many_sequences_of_any_length(T):
     assert np.allclose(scores.sum((1, 2)).cpu().numpy(), seen, rtol=1e-4, atol=1e-5)
 
 
+@pytest.mark.parametrize("B,T,H,H_kv,D,page,keys,dtype", [
+    (16, 24, 16, 4, 128, 128, 9000, "bf16"),   # one row tile
+    (2, 64, 40, 8, 128, 256, 30000, "bf16"),   # two row tiles and one
+    (2, 64, 32, 4, 64, 64, 30000, "fp16"),     # two row tiles twice
+    (12, 1, 16, 4, 128, 16, 7000, "fp16"),     # a few rows
+    (24, 9, 8, 8, 64, 32, 3000, "bf16"),       # many pieces a CTA
+])
+def test_long_ragged_batches_again_and_again(B, T, H, H_kv, D, page, keys, dtype):
+    """The whole GPU busy with sequences that end inside tiles, forty times without
+    a wait between: every pass the same bits, and the values of the plain form."""
+    rng = np.random.default_rng(keys)
+    lengths = [int(keys - rng.integers(0, keys // 2)) for _ in range(B)]
+    new = [max(1, T - int(rng.integers(0, 4))) for _ in range(B)]
+    st = Setup(lengths, T, H, H_kv, D, page, dtype, seed=keys, n_new=new)
+    caches = [st.cache() for _ in range(2)]
+    runs = [caches[i % 2].attend(st.q, st.tree, st.n_new) for i in range(40)]
+    for out, lse in runs[1:]:
+        assert torch.equal(out, runs[0][0]) and torch.equal(lse, runs[0][1])
+    scores = torch.zeros(B, H_kv, caches[0].capacity, device="cuda")
+    weights = [caches[0].weigh(st.q, runs[0][1], scores, st.tree, st.n_new, out=torch.zeros_like(scores)) for _ in range(20)]
+    assert all(torch.equal(w, weights[0]) for w in weights[1:])
+    assert caches[0].status() == 0 and caches[1].status() == 0
+    u, G = HALF_STEP[dtype], H // H_kv
+    for b in range(B):
+        n, m = lengths[b], new[b]
+        s = torch.arange(n + m, device="cuda")
+        at = st.table[b].long()[s // page], s % page
+        k, v, q = st.k[at].double(), st.v[at].double(), st.q[b, :m].double()
+        bits = (st.tree[b, :m, None] >> torch.arange(m, device="cuda")) & 1
+        seen = torch.cat((torch.ones(m, n, device="cuda"), bits), 1).bool()
+        x = torch.einsum("tkgd,jkd->tkgj", q.view(m, H_kv, G, D), k) * st.scale
+        x = x.masked_fill(~seen[:, None, None], -math.inf)
+        z = torch.logsumexp(x, -1)
+        p = torch.exp(x - z[..., None])
+        O = torch.einsum("tkgj,jkd->tkgd", p, v).reshape(m, H, D)
+        # the rounded weights' errors are independent: 8 of their standard deviations (u / sqrt 3 of sqrt(sum (p v)^2))
+        # and the common factor of the rounded sum, the result's own half step, and 2^-17 of the weights for fp32
+        spread = torch.einsum("tkgj,jkd->tkgd", p * p, v * v).sqrt().reshape(m, H, D)
+        norm = (p * p).sum(-1).sqrt().reshape(m, H, 1)
+        tol = 8 * u / 3 ** 0.5 * (spread + norm * O.abs()) + u * O.abs() + 2.0 ** -17 * v.abs().max() + \
+            ((n + m) * 2.0 ** -25 if dtype == "fp16" else 0)
+        err = (runs[0][0][b, :m].double() - O).abs()
+        assert (err <= tol).all(), (b, float((err - tol).max()))
+        assert (runs[0][0][b, m:] == 0).all()
+        w = (p * seen[:, None, None]).sum((0, 2)).T.float()
+        got = weights[0][b, :, :n + m].T
+        assert torch.allclose(got, w, rtol=2e-4, atol=1e-6)
+
+
 def test_a_cache_past_32_bits():
     """Element offsets of K and V past 2^32: a few pages at the far end of a large cache."""
     st = Setup([700, 90], 3, 4, 2, 128, 64, seed=60, spare=30)
