@@ -576,23 +576,23 @@ __global__ void __launch_bounds__(256) k_attend_join(const AttendParams p, int c
   float *lse = p.lse + (static_cast<int64_t>(b) * p.tok.H + h) * p.tok.T + t;
   const bool padding = t >= s.n;
   uint32_t c0 = 0, c1 = 0, units = 0;
-  int cost = 1;
+  int rg = 0;
   int64_t row_part = 0;
   // whether run c has key tiles of this row's item
   auto has = [&](uint32_t c) {
     const uint32_t z = min(runs.start(c + 1) - a, units), y = runs.start(c) > a ? runs.start(c) - a : 0u;
-    return first_tile(y, cost) < first_tile(z, cost);
+    return first_tile(s, y, rg) < first_tile(s, z, rg);
   };
   if (in && !padding) {
     // this row's item in the list: [a, a + units)
-    const int hk = h / p.tok.G, row = t * p.tok.G + h % p.tok.G, rg = row / (kTile * NX);
+    const int hk = h / p.tok.G, row = t * p.tok.G + h % p.tok.G;
+    rg = row / (kTile * NX);
     a += static_cast<uint32_t>(hk) * s.head_units() + s.group_start(rg);
     units = s.units(rg);
-    cost = s.cost(rg);
     c0 = runs.of(a);
     c1 = runs.of(a + units - 1);
-    if (NX == 2)
-      while (c1 > c0 && !has(c1)) --c1;
+    while (c0 < c1 && !has(c0)) ++c0;
+    while (c1 > c0 && !has(c1)) --c1;
     row_part = row - rg * kTile * NX;
   }
   const bool joined = c0 != c1;  // else one run has written the row
@@ -609,14 +609,14 @@ __global__ void __launch_bounds__(256) k_attend_join(const AttendParams p, int c
       return (static_cast<int64_t>(c) * 2 + slot) * (kTile * NX) + row_part;
     };
     for (uint32_t c = c0 + lane; c <= c1; c += 32)
-      if (NX == 1 || has(c)) M = fmaxf(M, p.part_ml[part_of(c)].x);
+      if (has(c)) M = fmaxf(M, p.part_ml[part_of(c)].x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
     const float Mu = M == -INFINITY ? 0.f : M;
     const uint32_t n = c1 - c0 + 1, z = c0 + n * (sub + 1) / WARPS;
 #pragma unroll 4
     for (uint32_t c = c0 + n * sub / WARPS; c < z; ++c) {
-      if (NX == 2 && !has(c)) continue;
+      if (!has(c)) continue;
       const int64_t part = part_of(c);
       const float4 ml = p.part_ml[part];
       const float f = exp2f(ml.x - Mu);

@@ -13,7 +13,11 @@ namespace bsa {
 // key tile of a group with two row tiles is 3, of one with a single one 2 (4240
 // against about 2700 clocks measured; with equal shares of tiles 2 sequences x 64
 // tokens x 5 heads a group, rows 256 + 64, over 75600 keys took 341 us, now 306),
-// where every group is alike 1.  With WHOLE, the list is of items instead, every
+// where every group is alike 1; and each item begins with kSwitch units of no tile,
+// for what changing to it costs the run's CTA (the sums and O of the item before, the
+// pipeline's refill: the CTAs with an item's start among their tiles were last by 6
+// of 34 us at 8 sequences x 1 token over 8192 keys, 42 us in all without, 39 with;
+// 2048 keys 27 and 22).  With WHOLE, the list is of items instead, every
 // row of the T * G in one, and a run takes each from its first tile to its last.
 constexpr int kAllRows = 0;
 
@@ -22,18 +26,20 @@ struct Seq {
   int len, n, tiles, groups;
   int last;  // the cost of a tile of the last group
   static constexpr int kCost = ROWS > kTile && !WHOLE ? 3 : 1;  // of the others
+  static constexpr int kSwitch = WHOLE ? 0 : ROWS > kTile ? 8 : 5;
   __device__ __forceinline__ int cost(int rg) const { return kCost == 1 ? 1 : rg == groups - 1 ? last : kCost; }
   // units of an item, and of a kv head
-  __device__ __forceinline__ uint32_t units(int rg) const { return WHOLE ? 1u : static_cast<uint32_t>(tiles) * cost(rg); }
+  __device__ __forceinline__ uint32_t units(int rg) const {
+    return WHOLE ? 1u : static_cast<uint32_t>(tiles) * cost(rg) + kSwitch;
+  }
   __device__ __forceinline__ uint32_t head_units() const {
     if (WHOLE) return groups;
-    if (kCost == 1) return static_cast<uint32_t>(tiles) * groups;
-    return groups == 0 ? 0u : static_cast<uint32_t>(tiles) * ((groups - 1) * kCost + last);
+    return groups == 0 ? 0u : static_cast<uint32_t>(tiles) * ((groups - 1) * kCost + cost(groups - 1)) + groups * kSwitch;
   }
   __device__ __forceinline__ uint32_t work(int H_kv) const { return H_kv * head_units(); }
   // the first unit of group rg within its kv head
   __device__ __forceinline__ uint32_t group_start(int rg) const {
-    return WHOLE ? rg : static_cast<uint32_t>(tiles) * kCost * rg;
+    return WHOLE ? rg : (static_cast<uint32_t>(tiles) * kCost + kSwitch) * rg;
   }
 };
 
@@ -104,7 +110,7 @@ __device__ __forceinline__ RunStart find_start(const CacheView &c, const TokenVi
       int item = 0, into = 0;
       if (here) {
         const uint32_t hk = off / s.head_units(), rest = off - hk * s.head_units();
-        const uint32_t other = WHOLE ? 1u : static_cast<uint32_t>(s.tiles) * s.kCost;
+        const uint32_t other = WHOLE ? 1u : static_cast<uint32_t>(s.tiles) * s.kCost + s.kSwitch;
         const int rg = min(static_cast<int>(rest / other), s.groups - 1);
         item = static_cast<int>(hk) * s.groups + rg;
         into = static_cast<int>(rest - s.group_start(rg));
@@ -129,8 +135,12 @@ __device__ __forceinline__ RunStart find_run(const CacheView &c, const TokenView
   return z > a ? find_start<ROWS, WHOLE>(c, t, a, static_cast<int>(z - a), lane) : RunStart{0, 0, 0, 0};
 }
 
-// The key tiles of the units [p0, p1) of an item: those that begin in them.
-__device__ __forceinline__ int first_tile(uint32_t p, int cost) { return static_cast<int>((p + cost - 1) / cost); }
+// The units [p0, p1) of an item hold the key tiles [first_tile(p0), first_tile(p1)).
+template <typename S>
+__device__ __forceinline__ int first_tile(const S &s, uint32_t p, int rg) {
+  const uint32_t x = p > S::kSwitch ? p - S::kSwitch : 0u;
+  return static_cast<int>(S::kCost == 1 ? x : (x + s.cost(rg) - 1) / s.cost(rg));
+}
 
 // One CTA's run, piece by piece (a piece: consecutive key tiles of one item).
 template <int ROWS, bool WHOLE = false>
@@ -154,8 +164,8 @@ struct Walk {
       hk = item / s.groups;
       rg = item % s.groups;
       const int units = static_cast<int>(s.units(rg)), end = min(units, at + left);
-      t0 = WHOLE ? 0 : first_tile(at, s.cost(rg));
-      t1 = WHOLE ? s.tiles : first_tile(end, s.cost(rg));
+      t0 = WHOLE ? 0 : first_tile(s, at, rg);
+      t1 = WHOLE ? s.tiles : first_tile(s, end, rg);
       whole = t0 == 0 && t1 == s.tiles;
       left -= end - at;
       at = 0;
