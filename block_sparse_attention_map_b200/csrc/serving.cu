@@ -98,15 +98,20 @@ bsa_status check_rope(const bsa_rope_spec *r, const bsa_tokens &t, bool empty, R
   return BSA_OK;
 }
 
-// Where the workspace's parts lie.
+// Where the workspace's parts lie (list_cap < 0: no lists).
 struct CacheWs {
   size_t scratch;                        // attend's pieces
   size_t count, to, from, mpos, mscore;  // evict's lists (they share the space: the calls follow one another)
   size_t total;
-  int list_cap;
 };
 
-CacheWs cache_ws(const CacheView &c, int budget) {
+// The entries of a head's lists: it moves at most min(budget, slots past the budget) slots.
+int moves_of(const CacheView &c, int budget) { return std::min(budget, std::max(c.capacity - budget, 0)); }
+
+// The most of any budget up to the given one.
+int most_moves(const CacheView &c, int budget) { return std::min(budget, c.capacity / 2); }
+
+CacheWs cache_ws(const CacheView &c, int list_cap) {
   CacheWs w{};
   const size_t heads = static_cast<size_t>(c.B) * c.H_kv;
   w.scratch = kHeaderBytes;
@@ -117,11 +122,9 @@ CacheWs cache_ws(const CacheView &c, int budget) {
     off += up256(bytes);
     return o;
   };
-  if (budget > 0) {
-    // a head moves at most min(budget, slots past the budget) slots
-    w.list_cap = std::min(budget, std::max(c.capacity - budget, 0));
+  if (list_cap >= 0) {
     w.count = take(4 * heads);
-    const size_t list = 4 * heads * static_cast<size_t>(w.list_cap);
+    const size_t list = 4 * heads * static_cast<size_t>(list_cap);
     w.to = take(list);
     w.from = take(list);
     w.mpos = take(list);
@@ -238,7 +241,7 @@ bsa_status bsa_cache_workspace_size(const bsa_cache *cache, int32_t budget, size
   CacheView c;
   const bsa_status st = check_cache(cache, &c);
   if (st != BSA_OK) return st;
-  *bytes = cache_ws(c, budget).total;
+  *bytes = cache_ws(c, budget > 0 ? most_moves(c, budget) : -1).total;
   return BSA_OK;
 }
 
@@ -289,7 +292,7 @@ bsa_status bsa_cache_attend(const bsa_cache *cache, const bsa_tokens *tok, const
   if (t.t.B == 0 || t.t.T == 0) return BSA_OK;
   if (q == nullptr || out == nullptr || lse == nullptr) return BSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned4(lse)) return BSA_ERR_UNSUPPORTED;
-  if ((st = check_ready(c, ws, ws_bytes, cache_ws(c, 0).total)) != BSA_OK) return st;
+  if ((st = check_ready(c, ws, ws_bytes, cache_ws(c, -1).total)) != BSA_OK) return st;
   c.status = static_cast<uint32_t *>(ws);
   AttendArgs a{};
   a.cache = c;
@@ -300,7 +303,7 @@ bsa_status bsa_cache_attend(const bsa_cache *cache, const bsa_tokens *tok, const
   copy3(a.os, t.qos);
   a.lse = lse;
   a.scale = t.t.scale;
-  a.scratch = static_cast<uint8_t *>(ws) + cache_ws(c, 0).scratch;
+  a.scratch = static_cast<uint8_t *>(ws) + cache_ws(c, -1).scratch;
   const bool fp16 = t.t.dtype == BSA_DTYPE_FP16;
   CUtensorMap tk, tv;
   if (!make_cache_map(&tk, c.k, c.n_pages, 1 << c.page_log, c.H_kv, c.D, c.ks, fp16) ||
@@ -321,7 +324,7 @@ bsa_status bsa_cache_weigh(const bsa_cache *cache, const bsa_tokens *tok, const 
   if (t.t.B == 0 || t.t.T == 0) return BSA_OK;
   if (q == nullptr || lse == nullptr || score_in == nullptr || score_out == nullptr) return BSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned4(lse) || !aligned4(score_in) || !aligned4(score_out)) return BSA_ERR_UNSUPPORTED;
-  if ((st = check_ready(c, ws, ws_bytes, cache_ws(c, 0).total)) != BSA_OK) return st;
+  if ((st = check_ready(c, ws, ws_bytes, cache_ws(c, -1).total)) != BSA_OK) return st;
   c.status = static_cast<uint32_t *>(ws);
   WeighArgs a{};
   a.cache = c;
@@ -353,7 +356,8 @@ bsa_status bsa_cache_evict(const bsa_cache *cache, const bsa_evict_spec *e, void
   if (!aligned4(e->next_pos) || !aligned4(e->score_in) || !aligned4(e->pos_in) || !aligned4(e->score_out) ||
       !aligned4(e->pos_out) || !aligned4(e->length_out))
     return BSA_ERR_UNSUPPORTED;
-  const CacheWs w = cache_ws(c, e->budget);
+  const int list_cap = moves_of(c, e->budget);
+  const CacheWs w = cache_ws(c, list_cap);
   if ((st = check_ready(c, ws, ws_bytes, w.total)) != BSA_OK) return st;
   uint8_t *base = static_cast<uint8_t *>(ws);
   c.status = reinterpret_cast<uint32_t *>(base);
@@ -368,7 +372,7 @@ bsa_status bsa_cache_evict(const bsa_cache *cache, const bsa_evict_spec *e, void
   a.score_out = e->score_out;
   a.pos_out = e->pos_out;
   a.length_out = e->length_out;
-  a.list_cap = w.list_cap;
+  a.list_cap = list_cap;
   a.count = reinterpret_cast<int32_t *>(base + w.count);
   a.to = reinterpret_cast<int32_t *>(base + w.to);
   a.from = reinterpret_cast<int32_t *>(base + w.from);

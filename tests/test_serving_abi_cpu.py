@@ -98,6 +98,19 @@ def test_workspace_sizes():
     assert size(cache(max_pages=1 << 26))[0] == 0 and size(cache(max_pages=(1 << 26) + 1))[0] == 2
 
 
+def test_a_workspace_of_one_budget_holds_every_smaller_one():
+    # capacity 32768 * 16: more slots can move at budget 2^18 than at any other
+    c, e = cache(max_pages=32768, B=16), sv.EvictSpec(10, 2, 3)
+    e.next_pos = e.score_in = e.pos_in = e.score_out = e.pos_out = e.length_out = 64
+    budgets = (1, 1000, 1 << 17, 1 << 18, 3 << 17, (1 << 19) - 1, 1 << 19, 1 << 20)
+    sizes = [size(c, n)[1] for n in budgets]
+    assert sizes == sorted(sizes)
+    for i, n in enumerate(sizes):
+        for small in budgets[:i + 1]:
+            e.budget = small
+            assert sv._fn("bsa_cache_evict")(c, e, 4096, n, None) == NODEV, (budgets[i], small)
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(n_pages=0), 1), (dict(page_size=0), 1), (dict(max_pages=0), 1), (dict(H_kv=0), 1), (dict(B=-1), 1),
     (dict(D=96), 2), (dict(dtype=2), 2), (dict(page_size=12), 2), (dict(page_size=4), 2), (dict(page_size=1 << 17), 2),
