@@ -11,7 +11,8 @@ namespace {
 constexpr size_t kHeaderBytes = 256;  // the status word's part of the workspace
 constexpr int kMaxTree = 64;          // new tokens a tree word can name
 constexpr int kMaxGroup = 128;
-constexpr int64_t kMaxTokens = int64_t{1} << 31;  // B * T * heads
+constexpr int64_t kMaxTokens = (int64_t{1} << 31) - (1 << 20);  // B * T * heads: a kernel's steps past them fit 31 bits
+constexpr int kMaxSequences = 1 << 16;  // of attend and weigh, whose CTAs and joined rows each read every length
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -190,7 +191,7 @@ bsa_status check_reading(const bsa_cache *cache, const bsa_tokens *tok, CacheVie
   if ((st = check_cache(cache, c)) != BSA_OK) return st;
   if ((st = check_tokens(tok, false, t)) != BSA_OK) return st;
   if (!matches(*cache, t->t) || t->t.T > kMaxTree) return BSA_ERR_INVALID_ARG;
-  if (t->t.H / t->t.H_kv > kMaxGroup) return BSA_ERR_UNSUPPORTED;
+  if (t->t.H / t->t.H_kv > kMaxGroup || c->B > kMaxSequences) return BSA_ERR_UNSUPPORTED;
   // units of work of all heads and row groups (up to 3 a tile): 31 bits
   const int64_t rows = static_cast<int64_t>(t->t.T) * (t->t.H / t->t.H_kv);
   if (static_cast<int64_t>(c->B) * c->H_kv * (c->capacity / kTile + 1) >= (int64_t{1} << 29) / (rows / kTile + 1))

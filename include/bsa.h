@@ -544,7 +544,7 @@ typedef struct bsa_evict_spec {
  * input and output do not overlap).  One launch, no workspace.
  * Errors: INVALID_ARG (null pointers, sizes, n_axes, n_pairs, layout or inverse
  * out of range), UNSUPPORTED (D, dtype, a stride not a multiple of 8 elements, a
- * tensor not 16-byte aligned), NO_DEVICE, CUDA.  B == 0 or T == 0: a checked no-op. */
+ * tensor not 16-byte aligned, B * T * H of 2^31 - 2^20 or more), NO_DEVICE, CUDA.  B == 0 or T == 0: a checked no-op. */
 BSA_API bsa_status bsa_rope(const bsa_tokens *tok, const bsa_rope_spec *rope, const void *q, void *q_out,
                             const void *k, void *k_out, bsa_stream_t stream);
 
@@ -573,7 +573,7 @@ BSA_API bsa_status bsa_cache_append(const bsa_cache *cache, const bsa_tokens *to
  * K and V of what a row does not see never reach it, NaN and infinities
  * included.  The same inputs give the same bits.
  * Errors as for bsa_cache_append; INVALID_ARG also for T > 64, UNSUPPORTED for
- * H / H_kv > 128 and for 2^29 or more tiles of 128 slots over all sequences, key
+ * H / H_kv > 128, for more than 65536 sequences and for 2^29 or more tiles of 128 slots over all sequences, key
  * heads and groups of 128 rows. */
 BSA_API bsa_status bsa_cache_attend(const bsa_cache *cache, const bsa_tokens *tok, const void *q, void *out,
                                     float *lse, void *ws, size_t ws_bytes, bsa_stream_t stream);

@@ -194,6 +194,17 @@ def test_calls_reject_bad_arguments_before_cuda(L):
     assert "cache" in L.bsa_status_string(11).decode()
 
 
+def test_limits_that_keep_the_kernels_counters_in_range():
+    # rows of a rotation: a block's step past the last one is added in 31 bits
+    rope, r = sv._fn("bsa_rope"), rope_spec()
+    for T, code in (((1 << 31) - (1 << 20), 2), ((1 << 31) - 1, 2), ((1 << 31) - (1 << 20) - 1, NODEV)):
+        assert rope(tokens(B=1, H=1, H_kv=1, T=T), r, 16, 32, 48, 64, None) == code
+    # sequences of the attention: its CTAs, and each joined row, read every length
+    for B, code in (((1 << 16) + 1, 2), (1 << 16, NODEV)):
+        assert sv._fn("bsa_cache_attend")(cache(B=B), tokens(B=B), 16, 32, 64, *WS, None) == code
+        assert sv._fn("bsa_cache_weigh")(cache(B=B), tokens(B=B), 16, 32, 64, 64, *WS, None) == code
+
+
 def test_tree_words():
     p = torch.tensor([[-1, 0, 0, 2, -1], [-1, -1, 1, 2, 3]])
     assert sv.tree_words(p).tolist() == [[1, 3, 5, 13, 16], [1, 2, 6, 14, 30]]
