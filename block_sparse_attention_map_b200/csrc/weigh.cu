@@ -50,7 +50,8 @@ struct WeighSmem {
                        bFinal = bQFull + 1, kNumBars = bFinal + 1;
   static constexpr int kLse = kBar + ((kNumBars * 8 + 15) & ~15);  // float [kRows] -lse * log2e
   static constexpr int kWord = kLse + kRows * 4;                    // uint64 [kMaxTok] tree words
-  static constexpr int kRun = kWord + kMaxTok * 8;
+  static constexpr int kAlive = kWord + kMaxTok * 8;                // uint32 [kRows / 32] rows that add anything (lse > -inf)
+  static constexpr int kRun = kAlive + kRows / 8;
   static constexpr int kMisc = kRun + 16;
   static constexpr int kAlloc = kMisc + 16;
 };
@@ -62,6 +63,7 @@ __global__ void __launch_bounds__(128 + kSumThreads, 1) k_weigh(const __grid_con
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::kBar);
   float *nlse = reinterpret_cast<float *>(sm + L::kLse);
   uint64_t *words = reinterpret_cast<uint64_t *>(sm + L::kWord);
+  uint32_t *alive = reinterpret_cast<uint32_t *>(sm + L::kAlive);
   RunStart *run_sm = reinterpret_cast<RunStart *>(sm + L::kRun);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::kMisc);
   int *abort_flag = reinterpret_cast<int *>(sm + L::kMisc + 4);
@@ -205,6 +207,8 @@ __global__ void __launch_bounds__(128 + kSumThreads, 1) k_weigh(const __grid_con
             z = x == -INFINITY ? -INFINITY : -x * kLog2e;
           }
           nlse[th] = z;
+          const uint32_t on = __ballot_sync(0xffffffffu, z != -INFINITY);
+          if (lane == 0) alive[th >> 5] = on;
         } else if (th - kRows < kMaxTok) {
           const int tok = th - kRows;
           words[tok] = tok < w.s.n ? tree_word(p.tok, w.b, tok, w.s.n) : 0ull;
@@ -224,35 +228,35 @@ __global__ void __launch_bounds__(128 + kSumThreads, 1) k_weigh(const __grid_con
           for (int half = 0; half < halves; ++half) {
             const float *zs = nlse + half * 128;
             const int cols = min(rows - half * 128, 128);
+            int fast = 0, c = 0;  // the columns [0, fast) all add something
+            if (!edge)
+              while (fast + 32 <= cols && alive[half * 4 + (fast >> 5)] == ~0u) fast += 32;
             if (!wwait(&bars[L::bSFull + y], used & 1)) { stop = true; break; }
             ++used;
             tc_fence_after();
-            int c = 0;
             uint32_t s[32];
-            if (!edge) {
 #pragma unroll 1
-              for (; c + 32 <= cols; c += 32) {
-                tmem_ld32(t_s + c, s);
-                tmem_wait_ld();
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                  const float4 z = *reinterpret_cast<const float4 *>(zs + c + 4 * q);
-                  const float2 e0 = __ffma2_rn(make_float2(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])), sc2,
-                                               make_float2(z.x, z.y));
-                  const float2 e1 = __ffma2_rn(make_float2(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])),
-                                               sc2, make_float2(z.z, z.w));
-                  acc[2 * (q & 1)] = __fadd2_rn(acc[2 * (q & 1)], make_float2(fast_exp2(e0.x), fast_exp2(e0.y)));
-                  acc[2 * (q & 1) + 1] = __fadd2_rn(acc[2 * (q & 1) + 1], make_float2(fast_exp2(e1.x), fast_exp2(e1.y)));
-                }
-              }
-            }
-            // the last columns, and tiles with new tokens: columns past the rows, and rows that do not see this
-            // thread's token, add nothing whatever they hold
-#pragma unroll 1
-            for (; c < cols; c += 32) {
+            for (; c < fast; c += 32) {
               tmem_ld32(t_s + c, s);
               tmem_wait_ld();
-              uint32_t on = cols - c >= 32 ? 0xffffffffu : (1u << (cols - c)) - 1u;
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const float4 z = *reinterpret_cast<const float4 *>(zs + c + 4 * q);
+                const float2 e0 = __ffma2_rn(make_float2(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])), sc2,
+                                             make_float2(z.x, z.y));
+                const float2 e1 = __ffma2_rn(make_float2(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])),
+                                             sc2, make_float2(z.z, z.w));
+                acc[2 * (q & 1)] = __fadd2_rn(acc[2 * (q & 1)], make_float2(fast_exp2(e0.x), fast_exp2(e0.y)));
+                acc[2 * (q & 1) + 1] = __fadd2_rn(acc[2 * (q & 1) + 1], make_float2(fast_exp2(e1.x), fast_exp2(e1.y)));
+              }
+            }
+            // the last columns, tiles with new tokens, and rows that add nothing: columns past the rows, rows whose lse
+            // is -inf, and rows that do not see this thread's token, whatever they hold
+#pragma unroll 1
+            for (; c < cols; c += 32) {
+              uint32_t on = alive[half * 4 + (c >> 5)];
+              tmem_ld32(t_s + c, s);
+              tmem_wait_ld();
               if (edge && d >= 0) {
                 // the columns of the tokens that see new token d
                 const int first = row0 + half * 128 + c;

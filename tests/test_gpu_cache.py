@@ -237,6 +237,31 @@ def test_words_that_leave_rows_empty_and_bits_past_the_new_tokens():
     assert np.allclose(total, [3 * 4, 3 * 4, 1 * 4], rtol=1e-5)  # every row that sees something spreads a weight of 1
 
 
+@pytest.mark.parametrize("T,H,H_kv,lengths", [(1, 2, 2, [300]), (16, 20, 2, [300, 40]), (64, 10, 2, [513, 0])])
+def test_rows_whose_lse_is_minus_infinity_weigh_nothing_whatever_they_hold(T, H, H_kv, lengths):
+    st = Setup(lengths, T, H, H_kv, 64, 16, seed=30 + T)
+    cache = st.cache()
+    _, lse = cache.attend(st.q, st.tree)
+    off = torch.rand(lse.shape, generator=st.g, device="cuda") < 0.3
+    off[0, -1] = True  # a whole head
+    lse = lse.masked_fill(off, -math.inf)
+    rows = off.transpose(1, 2)[..., None]
+    plain, odd = st.q.masked_fill(rows, 0.0), st.q.masked_fill(rows, math.nan)
+    odd[..., 1::2] = odd[..., 1::2].masked_fill(rows, math.inf)
+    scores = torch.rand(st.B, H_kv, cache.capacity, generator=st.g, device="cuda")
+    a, b = torch.empty_like(scores), torch.empty_like(scores)
+    cache.weigh(plain, lse, scores, st.tree, out=a)
+    cache.weigh(odd, lse, scores, st.tree, out=b)
+    want = oracle.weigh(f64(scores), f64(plain), st.seqs(), f64(lse), st.lengths, st.new, words(st), st.scale)
+    e = exponent_tolerance(f64(plain), st.seqs(), st.scale)
+    for i in range(st.B):
+        n = st.lengths[i] + st.new[i]
+        assert torch.equal(a[i, :, :n], b[i, :, :n])
+        w = want[i, :, :n]
+        tol = (w - f64(scores)[i, :, :n]) * (2 * e + T * (H // H_kv) * 2.0 ** -23) + 2.0 ** -23 * w + 1e-12
+        assert (np.abs(f64(b)[i, :, :n] - w) <= tol).all()
+
+
 def test_strided_tensors_another_scale_and_a_shared_page():
     st = Setup([70, 75], 5, 4, 2, 64, 16, seed=11)
     big = torch.full((st.k.shape[0], 2, 2, 16, 192), math.nan, dtype=torch.bfloat16, device="cuda")
