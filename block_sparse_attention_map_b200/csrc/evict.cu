@@ -137,7 +137,8 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) k_evict_selec
   const int32_t *pos = a.pos_in + base;
   float *score_out = a.score_out + base;
   int32_t *pos_out = a.pos_out + base;
-  pdl_trigger();
+  // only this call's second kernel may start under it: another's may not expect it
+  if (!MOVES || a.length_out == a.cache.length) pdl_trigger();
   if (MOVES && a.length_out != a.cache.length && head % a.cache.H_kv == 0 && rank == 0 && tid == 0)
     a.length_out[b] = min(n, a.budget);
   if (n <= a.budget) {  // the whole cluster
