@@ -73,16 +73,24 @@ def _stream_of(index):
     return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
 
-def _call(name, index, *args):
-    """One library call on the current stream of device ``index``, with it current."""
+def _call(name, index, stream, *args):
+    """One library call on this stream of device ``index``, with the device current."""
     fn = _FNS.get(name) or _fn(name)
     if index == torch.cuda.current_device():
-        rc = fn(*args, _stream_of(index))
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(index):
-            rc = fn(*args, _stream_of(index))
+            rc = fn(*args, stream)
     if rc != 0:
         raise BsaError(rc, name)
+
+
+def _int32(x, name):
+    """An int that the library's int32 holds (ctypes would drop the bits above)."""
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name}: {x} does not fit 32 bits")
+    return x
 
 
 def _strides(shape, stride, name):
@@ -224,7 +232,7 @@ def _rotate(q, k, pos, inv_freq, axis, layout, inverse, q_out, k_out):
         _check_apart(qp, qop, *qa, "q_out")
     if ka is not None:
         _check_apart(kp, kop, *ka, "k_out")
-    _call("bsa_rope", index, t, _rope_args(r, pos, inv_freq, axis), qp, qop, kp, kop)
+    _call("bsa_rope", index, _stream_of(index), t, _rope_args(r, pos, inv_freq, axis), qp, qop, kp, kop)
     return q_out, k_out
 
 
@@ -289,24 +297,51 @@ def _append_layout(ks, kt, vs, vt, qs, qt, qos, qot, ps, pt, fs, axs, layout, B,
 class CacheWorkspace:
     """Scratch memory and the sticky status word of paged caches' calls.  Caches
     whose calls all follow one another on one stream (the layers of a model) may
-    share one; it grows to what the largest call needs."""
+    share one; it grows to what the largest call needs.  A captured graph goes on
+    with the memory it was captured with, which the workspace keeps: keep the
+    workspace (or a PagedCache that has it) as long as the graph."""
 
     def __init__(self, device):
         self.device = torch.device(device)
-        self.buf, self.ptr, self.nbytes = None, None, 0
+        if self.device.type != "cuda":
+            raise ValueError("workspace: expected a CUDA device")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.bufs, self.ptr, self.nbytes = [], None, 0  # the last buffer is the one in use
+        self.streams = set()                            # that it is in use on
 
     def grow(self, nbytes):
-        """At least ``nbytes``, the status word kept."""
+        """At least ``nbytes``."""
         if nbytes <= self.nbytes:
             return
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("the workspace cannot grow while a stream is captured: reserve() before the capture")
-        new = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        if self.buf is None:
+        with torch.cuda.device(self.device):
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("the workspace cannot grow while a stream is captured: reserve() before the capture")
+            nbytes = max(nbytes, 2 * self.nbytes)  # so that those that are kept are less than the one in use
+            new = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
             new[:256].zero_()
-        else:
-            new[:256].copy_(self.buf[:256])
-        self.buf, self.ptr, self.nbytes = new, new.data_ptr(), nbytes
+        self.bufs.append(new)
+        self.ptr, self.nbytes, self.streams = new.data_ptr(), nbytes, {_stream_of(self.device.index)}
+
+    def use(self, stream):
+        """The current stream, of this handle, uses the memory from now on."""
+        self.bufs[-1].record_stream(torch.cuda.current_stream(self.device))
+        self.streams.add(stream)
+
+    def status(self, clear):
+        with torch.cuda.device(self.device):
+            stream = _stream_of(self.device.index)
+            found = [int(lib().bsa_get_device_status(x.data_ptr(), x.numel(), stream, 1 if clear else 0))
+                     for x in reversed(self.bufs)]
+        return next((x for x in found if x != 0), 0)
+
+
+def _held(i, name):
+    """A tensor whose address the library holds: another cannot take its place (``x.length += 1`` works in place)."""
+    def keep(self, value):
+        if value is not self._tensors[i]:
+            raise ValueError(f"{name}: change the tensor in place, or make another PagedCache")
+    return property(lambda self: self._tensors[i], keep)
 
 
 class PagedCache:
@@ -331,7 +366,7 @@ class PagedCache:
             raise ValueError("v must have k's shape")
         self.device, self.dtype, self._index = k.device, k.dtype, k.get_device()
         _rows(v, "v", self._index, self.dtype)
-        self.k, self.v, self.page_table, self.length = k, v, page_table, length
+        self._tensors = k, v, page_table, length
         self.n_pages, self.page_size, self.H_kv, self.D = k.shape
         if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.get_device() != self._index or \
                 (page_table.shape[1] > 1 and page_table.stride(1) != 1):
@@ -348,15 +383,28 @@ class PagedCache:
         self.workspace = CacheWorkspace(self.device) if workspace is None else workspace
         if self.workspace.device != self.device:
             raise ValueError("workspace: on another device")
-        self._reserved = set()  # budgets the workspace holds
+        self._reserved = 0  # the largest budget whose lists the workspace holds
         self.reserve(0)
 
+    k = _held(0, "k")
+    v = _held(1, "v")
+    page_table = _held(2, "page_table")
+    length = _held(3, "length")
+
     def reserve(self, budget):
-        """Grows the workspace to what evictions to ``budget`` need."""
+        """Grows the workspace to what evictions to ``budget`` or less need."""
         n = ctypes.c_size_t(0)
+        budget = _int32(budget, "budget")
         _check(_fn("bsa_cache_workspace_size")(self._c, budget, ctypes.byref(n)), "bsa_cache_workspace_size")
         self.workspace.grow(n.value)
-        self._reserved.add(budget)
+        self._reserved = max(self._reserved, budget)
+
+    def _run(self, name, *args):
+        """A library call on the cache, on the current stream."""
+        ws, stream = self.workspace, _stream_of(self._index)
+        if stream not in ws.streams:
+            ws.use(stream)
+        _call(name, self._index, stream, self._c, *args, ws.ptr, ws.nbytes)
 
     def _token_layout(self, shape, stride, out_shape, out_stride, scale):
         if len(shape) != 4 or shape[3] != self.D:
@@ -416,7 +464,7 @@ class PagedCache:
             _check_apart(qp, qop, *qa, "q_out")
         if rp is not None:
             r = _rope_args(rp, pos, inv_freq, axis)
-        _call("bsa_cache_append", index, self._c, t, r, qp, qop, k.data_ptr(), v.data_ptr(), self.workspace.ptr, self.workspace.nbytes)
+        self._run("bsa_cache_append", t, r, qp, qop, k.data_ptr(), v.data_ptr())
         return q_out
 
     def attend(self, q, tree=None, n_new=None, scale=None, out=None, lse=None):
@@ -433,8 +481,7 @@ class PagedCache:
         B, T, H, _ = q.shape
         if lse is None:
             lse = torch.empty(B, H, T, dtype=torch.float32, device=self.device)
-        _call("bsa_cache_attend", self._index, self._c, t, q.data_ptr(), out.data_ptr(),
-              _flat(lse, "lse", self._index, torch.float32, (B, H, T)), self.workspace.ptr, self.workspace.nbytes)
+        self._run("bsa_cache_attend", t, q.data_ptr(), out.data_ptr(), _flat(lse, "lse", self._index, torch.float32, (B, H, T)))
         return out, lse
 
     def weigh(self, q, lse, scores, tree=None, n_new=None, scale=None, out=None):
@@ -447,8 +494,8 @@ class PagedCache:
         shape = (B, self.H_kv, self.capacity)
         score_in = _flat(scores, "scores", self._index, torch.float32, shape)
         score_out = score_in if out is None else _flat(out, "out", self._index, torch.float32, shape)
-        _call("bsa_cache_weigh", self._index, self._c, t, q.data_ptr(),
-              _flat(lse, "lse", self._index, torch.float32, (B, H, T)), score_in, score_out, self.workspace.ptr, self.workspace.nbytes)
+        self._run("bsa_cache_weigh", t, q.data_ptr(), _flat(lse, "lse", self._index, torch.float32, (B, H, T)), score_in,
+                  score_out)
         return scores if out is None else out
 
     def evict(self, scores, pos, next_pos, budget, sinks=0, recent=0, scores_out=None, pos_out=None,
@@ -464,7 +511,7 @@ class PagedCache:
         scores_out = scores if scores_out is None else scores_out
         pos_out = pos if pos_out is None else pos_out
         length_out = self.length if length_out is None else length_out
-        e = EvictSpec(int(budget), int(sinks), int(recent))
+        e = EvictSpec(_int32(budget, "budget"), _int32(sinks, "sinks"), _int32(recent, "recent"))
         index = self._index
         e.next_pos = _flat(next_pos, "next_pos", index, torch.int32, (self.B,))
         e.score_in = _flat(scores, "scores", index, torch.float32, shape)
@@ -472,12 +519,11 @@ class PagedCache:
         e.score_out = e.score_in if scores_out is scores else _flat(scores_out, "scores_out", index, torch.float32, shape)
         e.pos_out = e.pos_in if pos_out is pos else _flat(pos_out, "pos_out", index, torch.int32, shape)
         e.length_out = _flat(length_out, "length_out", index, torch.int32, (self.B,))
-        if e.budget not in self._reserved:
-            self.reserve(max(e.budget, 0))
-        _call("bsa_cache_evict", index, self._c, e, self.workspace.ptr, self.workspace.nbytes)
+        if e.budget > self._reserved:
+            self.reserve(e.budget)
+        self._run("bsa_cache_evict", e)
         return scores_out, pos_out, length_out
 
     def status(self, clear=False):
         """The sticky device status of this cache's calls (0: ok; synchronises)."""
-        with torch.cuda.device(self._index):
-            return int(lib().bsa_get_device_status(self.workspace.ptr, self.workspace.nbytes, _stream_of(self._index), 1 if clear else 0))
+        return self.workspace.status(clear)

@@ -633,6 +633,58 @@ def test_caches_may_share_a_workspace():
     assert b.status(clear=True) == 11 and got[0].shape == st.q.shape
 
 
+def test_a_captured_graph_keeps_its_workspace_when_the_cache_takes_a_larger_one():
+    st = Setup([300, 40], 2, 4, 2, 64, 16, seed=71)
+    cache = st.cache()
+    want = cache.attend(st.q, st.tree)
+    torch.cuda.synchronize()
+    graph, at, nbytes = torch.cuda.CUDAGraph(), cache.workspace.ptr, cache.workspace.nbytes
+    with torch.cuda.graph(graph):
+        got = cache.attend(st.q, st.tree)
+    cache.workspace.grow(nbytes + 1)
+    assert cache.workspace.ptr != at
+    # whatever is allocated now is not the graph's
+    others = [torch.full((nbytes,), 7, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert all(x.data_ptr() + nbytes <= at or at + nbytes <= x.data_ptr() for x in others)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert all((x == 7).all() for x in others)
+    # and its errors are seen
+    st.table[0, 0] = -1
+    graph.replay()
+    assert cache.status(clear=True) == 11 and cache.status() == 0
+
+
+def test_a_workspace_outlives_its_cache_on_another_stream():
+    st = Setup([3000, 4000], 4, 8, 2, 128, 128, seed=72)
+    want = st.cache().attend(st.q, st.tree)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(8):
+        cache = st.cache()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                got = cache.attend(st.q, st.tree)
+        n = cache.workspace.nbytes
+        del cache
+        scribble = torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # on the stream the workspace came from
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and (scribble == 255).all()
+
+
+def test_a_cache_holds_the_tensors_it_was_made_with():
+    st = Setup([20, 30], 3, 4, 2, 64, 16, seed=73)
+    cache = st.cache()
+    at = cache.length.data_ptr()
+    cache.length += 1
+    assert cache.length.data_ptr() == at and cache.length.tolist() == [21, 31]
+    for name in ("k", "v", "page_table", "length"):
+        with pytest.raises(ValueError):
+            setattr(cache, name, getattr(cache, name) + 1)
+
+
 def test_refusals():
     st = Setup([20, 30], 3, 4, 2, 64, 16, seed=40)
     cache = st.cache()
