@@ -148,7 +148,10 @@ def _rope_layout(B, T, shape, stride, n, layout, inverse):
     r = RopeSpec(shape[0], n, LAYOUT[layout], 1 if inverse else 0)
     r.pos_stride[:] = stride[:2]
     if stride[0] == 0 and stride[1] == 0 and shape[0] * B > 1:
-        raise ValueError("pos: give every axis or sequence its row (a fully broadcast pos is not taken)")
+        # zeros would mean contiguous to the library; an axis or sequence there is one of may have any stride
+        if shape[0] > 1 and B > 1:
+            raise ValueError("pos: give every axis or every sequence its own rows (one row for all is not taken)")
+        r.pos_stride[0 if shape[0] == 1 else 1] = 1
     return r
 
 
@@ -171,7 +174,13 @@ def _rope_args(proto, pos, inv_freq, axis):
 def _check_apart(a, b, same, span_x, span_out, name):
     """An output at address ``b`` is its input at ``a`` itself (``same`` strides) or shares no memory with it."""
     if a < b + 2 * span_out and b < a + 2 * span_x and not (a == b and same):
-        raise ValueError(f"{name}: overlaps its input without being it")
+        raise ValueError(f"{name}: overlaps an input without being it")
+
+
+def _check_flat(a, b, nbytes, name):
+    """As :func:`_check_apart` for two contiguous tensors of one size."""
+    if a < b + nbytes and b < a + nbytes and a != b:
+        raise ValueError(f"{name}: overlaps an input without being it")
 
 
 def _pair_layout(xs, xt, os, ot, name):
@@ -232,6 +241,14 @@ def _rotate(q, k, pos, inv_freq, axis, layout, inverse, q_out, k_out):
         _check_apart(qp, qop, *qa, "q_out")
     if ka is not None:
         _check_apart(kp, kop, *ka, "k_out")
+        if qa is not None:
+            # in place, q and k (and both outputs) may lie side by side in one tensor, each head its own
+            if qop != qp:
+                _check_apart(kp, qop, False, ka[1], qa[2], "q_out")
+            if kop != kp:
+                _check_apart(qp, kop, False, qa[1], ka[2], "k_out")
+            if qop == kop and qa[2] > 0:
+                raise ValueError("q_out and k_out are one tensor")
     _call("bsa_rope", index, _stream_of(index), t, _rope_args(r, pos, inv_freq, axis), qp, qop, kp, kop)
     return q_out, k_out
 
@@ -281,6 +298,7 @@ def _append_layout(ks, kt, vs, vt, qs, qt, qos, qot, ps, pt, fs, axs, layout, B,
     t = Tokens(B, T, H_kv, H_kv, D, dtype)
     t.k_stride[:], t.v_stride[:] = _strides(ks, kt, "k"), _strides(vs, vt, "v")
     q = r = None
+    spans = _span(ks, kt), _span(vs, vt)
     if qs is not None:
         q = _pair_layout(qs, qt, qos, qot, "q")
         if qs[0] != B or qs[1] != T or qs[3] != D:
@@ -291,7 +309,7 @@ def _append_layout(ks, kt, vs, vt, qs, qt, qos, qot, ps, pt, fs, axs, layout, B,
         if len(fs) != 1 or axs != fs:
             raise ValueError("inv_freq and axis: expected one entry a pair")
         r = _rope_layout(B, T, ps, pt, fs[0], layout, False)
-    return t, r, q and q[2:]
+    return t, r, q and q[2:], spans
 
 
 class CacheWorkspace:
@@ -418,14 +436,17 @@ class PagedCache:
         t.qo_stride[:] = _strides(out_shape, out_stride, "out")
         if scale is not None:
             t.scale = scale
-        return t
+        return t, _span(shape, stride), _span(out_shape, out_stride)
 
     def _queries(self, q, out, tree, n_new, scale):
         """The argument block of q [B, T, H, D] and its options, checked."""
         shape, stride, out_shape, out_stride = q.shape, q.stride(), out.shape, out.stride()
-        t = Tokens.from_buffer_copy(_layout(
+        proto, span_q, span_out = _layout(
             ("t", shape, stride, out_shape, out_stride, scale, self.B, self.H_kv, self.D, self._c.dtype),
-            lambda: self._token_layout(shape, stride, out_shape, out_stride, scale)))
+            lambda: self._token_layout(shape, stride, out_shape, out_stride, scale))
+        t = Tokens.from_buffer_copy(proto)
+        if out is not q:  # the rows of one token are written while others' are still to be read
+            _check_apart(q.data_ptr(), out.data_ptr(), False, span_q, span_out, "out")
         if q.dtype != self.dtype or q.get_device() != self._index:
             raise ValueError(f"q: expected a {self.dtype} tensor on cuda:{self._index}")
         if n_new is not None:
@@ -456,15 +477,19 @@ class PagedCache:
             ps, pt, fs, axs = pos.shape, pos.stride(), inv_freq.shape, axis.shape
         args = (k.shape, k.stride(), v.shape, v.stride(), qs, qt, qos, qot, ps, pt, fs, axs, layout, self.B, self.H_kv, self.D,
                 self._c.dtype)
-        proto, rp, qa = _layout(args, lambda: _append_layout(*args))
+        proto, rp, qa, spans = _layout(args, lambda: _append_layout(*args))
+        kp, vp = k.data_ptr(), v.data_ptr()
         t = Tokens.from_buffer_copy(proto)
         if n_new is not None:
             t.n_new = _flat(n_new, "n_new", index, torch.int32, (self.B,))
         if qa is not None:
             _check_apart(qp, qop, *qa, "q_out")
+            if qop != qp:
+                _check_apart(kp, qop, False, spans[0], qa[2], "q_out")
+                _check_apart(vp, qop, False, spans[1], qa[2], "q_out")
         if rp is not None:
             r = _rope_args(rp, pos, inv_freq, axis)
-        self._run("bsa_cache_append", t, r, qp, qop, k.data_ptr(), v.data_ptr())
+        self._run("bsa_cache_append", t, r, qp, qop, kp, vp)
         return q_out
 
     def attend(self, q, tree=None, n_new=None, scale=None, out=None, lse=None):
@@ -475,6 +500,8 @@ class PagedCache:
         ``n_new`` are written as 0 / -inf."""
         if out is None:
             out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
+        elif out is q:
+            raise ValueError("out: overlaps q")
         t = self._queries(q, out, tree, n_new, scale)
         if out.dtype != self.dtype or out.get_device() != self._index:
             raise ValueError(f"out: expected a {self.dtype} tensor on cuda:{self._index}")
@@ -493,7 +520,10 @@ class PagedCache:
         B, T, H, _ = q.shape
         shape = (B, self.H_kv, self.capacity)
         score_in = _flat(scores, "scores", self._index, torch.float32, shape)
-        score_out = score_in if out is None else _flat(out, "out", self._index, torch.float32, shape)
+        score_out = score_in
+        if out is not None:
+            score_out = _flat(out, "out", self._index, torch.float32, shape)
+            _check_flat(score_in, score_out, 4 * out.numel(), "out")
         self._run("bsa_cache_weigh", t, q.data_ptr(), _flat(lse, "lse", self._index, torch.float32, (B, H, T)), score_in,
                   score_out)
         return scores if out is None else out
@@ -519,6 +549,16 @@ class PagedCache:
         e.score_out = e.score_in if scores_out is scores else _flat(scores_out, "scores_out", index, torch.float32, shape)
         e.pos_out = e.pos_in if pos_out is pos else _flat(pos_out, "pos_out", index, torch.int32, shape)
         e.length_out = _flat(length_out, "length_out", index, torch.int32, (self.B,))
+        nbytes = 4 * self.B * self.H_kv * self.capacity
+        if nbytes > 0:  # (an address of 0 reads as None)
+            if scores_out is not scores:
+                _check_flat(e.score_in, e.score_out, nbytes, "scores_out")
+            if pos_out is not pos:
+                _check_flat(e.pos_in, e.pos_out, nbytes, "pos_out")
+            if length_out is not self.length:
+                _check_flat(self._c.length, e.length_out, 4 * self.B, "length_out")
+                if abs(e.length_out - e.next_pos) < 4 * self.B:
+                    raise ValueError("length_out: overlaps next_pos")
         if e.budget > self._reserved:
             self.reserve(e.budget)
         self._run("bsa_cache_evict", e)

@@ -506,7 +506,7 @@ typedef struct bsa_tokens {
  * page index outside [0, n_pages) reads as zeros and is never written.  Slots
  * that are not in use may hold anything, NaN included.  Sequences may share
  * pages that are only read; append and evict write in place, so the pages they
- * write belong to one sequence. */
+ * write belong to one sequence, once. */
 typedef struct bsa_cache {
   int32_t n_pages;         /* 1 .. 2^30                                           */
   int32_t page_size;       /* slots per page: a power of two, 8 .. 65536           */
@@ -531,17 +531,17 @@ typedef struct bsa_evict_spec {
   int32_t recent;          /* keep pos >= next_pos[b] - recent                    */
   int32_t reserved;
   const int32_t *next_pos; /* device [B]: the position of the sequence's next token */
-  /* device [B, H_kv, capacity]; the outputs may be the inputs */
+  /* device [B, H_kv, capacity]; an output is its input or apart from it */
   const float *score_in;
   const int32_t *pos_in;
   float *score_out;
   int32_t *pos_out;
-  int32_t *length_out;     /* device [B]; may be the cache's length               */
+  int32_t *length_out;     /* device [B]; the cache's length or apart from it      */
 } bsa_evict_spec;
 
 /* Rotates q [B, T, H, D] into q_out and k [B, T, H_kv, D] into k_out, either
  * pair NULL to leave it out (q_out = q and k_out = k rotate in place; otherwise
- * input and output do not overlap).  One launch, no workspace.
+ * no output overlaps an input or the other output).  One launch, no workspace.
  * Errors: INVALID_ARG (null pointers, sizes, n_axes, n_pairs, layout or inverse
  * out of range), UNSUPPORTED (D, dtype, a stride not a multiple of 8 elements, a
  * tensor not 16-byte aligned, B * T * H of 2^31 - 2^20 or more), NO_DEVICE, CUDA.  B == 0 or T == 0: a checked no-op. */
@@ -568,7 +568,8 @@ BSA_API bsa_status bsa_cache_append(const bsa_cache *cache, const bsa_tokens *to
 /* Attention of T <= 64 new tokens (a tree of drafted tokens, or one) over the
  * cache, which holds them already: token t of sequence b sees the slots below
  * length[b] and the new tokens its tree word names (bits at or past n_new[b]
- * are ignored).  out [B, T, H, D] (qo_stride), lse fp32 [B, H, T] contiguous.
+ * are ignored).  out [B, T, H, D] (qo_stride; it does not overlap q), lse fp32
+ * [B, H, T] contiguous.
  * A row that sees nothing, and every row t >= n_new[b], is written as 0 / -inf.
  * K and V of what a row does not see never reach it, NaN and infinities
  * included.  The same inputs give the same bits.
@@ -581,8 +582,8 @@ BSA_API bsa_status bsa_cache_attend(const bsa_cache *cache, const bsa_tokens *to
 /* Accumulated attention weight: for every slot j < length[b] + n_new[b] and key
  * head, score_out = score_in + the sum over the tokens t < n_new[b] and the
  * query heads h of the group that see j of exp(scale q.k_j - lse[b, h, t]).
- * score [B, H_kv, capacity] fp32 (score_out may be score_in; other slots are
- * left as they are); lse as bsa_cache_attend wrote it (-inf: the row adds
+ * score [B, H_kv, capacity] fp32 (score_out is score_in or apart from it; other
+ * slots are left as they are); lse as bsa_cache_attend wrote it (-inf: the row adds
  * nothing).  The same inputs give the same bits.  Errors as for
  * bsa_cache_attend. */
 BSA_API bsa_status bsa_cache_weigh(const bsa_cache *cache, const bsa_tokens *tok, const void *q,

@@ -720,6 +720,34 @@ def test_refusals():
         assert e.value.code == code
 
 
+def test_outputs_that_overlap_inputs_are_refused():
+    st = Setup([20, 30], 3, 4, 2, 64, 16, seed=42)
+    cache = st.cache()
+    lse = cache.attend(st.q, st.tree)[1]
+    wide = torch.zeros(2, 4, 4, 64, dtype=torch.bfloat16, device="cuda")
+    n = 2 * 2 * cache.capacity
+    buf, ibuf = torch.zeros(n + 8, device="cuda"), torch.zeros(n + 8, dtype=torch.int32, device="cuda")
+    shape = (2, 2, cache.capacity)
+    sc, sc2, ps, ps2 = buf[:n].view(shape), buf[8:].view(shape), ibuf[:n].view(shape), ibuf[8:].view(shape)
+    both = torch.zeros(3, dtype=torch.int32, device="cuda")
+    nxt = torch.zeros(2, dtype=torch.int32, device="cuda")
+    kv = st.q[:, :, :2].contiguous()
+    for call in (lambda: cache.attend(st.q, out=st.q), lambda: cache.attend(st.q, out=st.q.view(st.q.shape)),
+                 lambda: cache.attend(wide[:, :3], out=wide[:, 1:]), lambda: cache.weigh(st.q, lse, sc, out=sc2),
+                 lambda: cache.evict(sc, ps, nxt, 4, scores_out=sc2), lambda: cache.evict(sc, ps, nxt, 4, pos_out=ps2),
+                 lambda: cache.evict(sc, ps, nxt, 4, length_out=nxt), lambda: cache.evict(sc, ps, both[:2], 4, length_out=both[1:]),
+                 lambda: cache.append(kv, kv.clone(), q=kv.clone(), q_out=kv),
+                 lambda: cache.append(kv.clone(), kv, q=kv.clone(), q_out=kv),
+                 lambda: cache.evict(sc, ps, nxt, 1 << 32), lambda: cache.evict(sc, ps, nxt, 4, sinks=1 << 32),
+                 lambda: cache.evict(sc, ps, nxt, 4, recent=(1 << 32) + 1), lambda: cache.reserve(1 << 32)):
+        with pytest.raises(ValueError):
+            call()
+    # in place by another view of the same memory is in place
+    before = cache.length.clone()
+    cache.evict(sc, ps, nxt, 4, scores_out=sc.view(shape), pos_out=ps.view(shape), length_out=cache.length.view(2))
+    assert before.tolist() == [20, 30] and cache.length.tolist() == [4, 4] and cache.status() == 0
+
+
 def test_empty_calls_do_nothing():
     st = Setup([20, 30], 0, 4, 2, 64, 16, seed=41)
     cache = st.cache()

@@ -219,6 +219,43 @@ def test_refusals():
     assert e.value.code == 2
 
 
+def test_outputs_across_each_other_are_refused_and_packed_ones_are_not():
+    g = gen(9)
+    pos = torch.arange(5, device="cuda", dtype=torch.int32).view(1, 1, 5)
+    freq, axis = tables(32, 1)
+    qk = normal(g, (1, 5, 6, 64), "bf16")
+    q, k = qk[:, :, :3], qk[:, :, 3:]
+    want = bsa.rope(q, k, pos, freq, axis)
+    a, b, c = torch.empty_like(want[0]), torch.empty_like(want[0]), q.contiguous()
+    for kw in (dict(q=q, k=k, q_out=k, k_out=q), dict(q=q, k=k, q_out=a, k_out=a), dict(q=c, k=b, q_out=b, k_out=a),
+               dict(q=c, k=b, q_out=a, k_out=c)):
+        with pytest.raises(ValueError):
+            bsa.rope(kw["q"], kw["k"], pos, freq, axis, q_out=kw["q_out"], k_out=kw["k_out"])
+    packed = torch.empty_like(qk)
+    bsa.rope(q, k, pos, freq, axis, q_out=packed[:, :, :3], k_out=packed[:, :, 3:])
+    bsa.rope(q, k, pos, freq, axis, q_out=q, k_out=k)
+    for got in (packed, qk):
+        assert torch.equal(got[:, :, :3], want[0]) and torch.equal(got[:, :, 3:], want[1])
+
+
+def test_positions_that_sequences_or_axes_share():
+    g = gen(10)
+    q = normal(g, (3, 5, 2, 64), "bf16")
+    row = torch.randint(0, 9000, (5,), generator=g, device="cuda", dtype=torch.int32)
+    freq, axis = tables(32, 1)
+    want = bsa.rope(q, None, row.expand(1, 3, 5).contiguous(), freq, axis)[0]
+    assert torch.equal(bsa.rope(q, None, row.expand(1, 3, 5), freq, axis)[0], want)
+    f2, a2 = tables(32, 2)
+    want = bsa.rope(q[:1], None, row.expand(2, 1, 5).contiguous(), f2, a2)[0]
+    assert torch.equal(bsa.rope(q[:1], None, row.expand(2, 1, 5), f2, a2)[0], want)
+    two = torch.stack([row, row + 7])
+    for pos in (two[:, None].expand(2, 3, 5), two[None].expand(2, 2, 5)):
+        x = q[:pos.shape[1]]
+        assert torch.equal(bsa.rope(x, None, pos, f2, a2)[0], bsa.rope(x, None, pos.contiguous(), f2, a2)[0])
+    with pytest.raises(ValueError):
+        bsa.rope(q, None, row.expand(2, 3, 5), f2, a2)
+
+
 def test_empty_calls_do_nothing():
     freq, axis = tables(32, 1)
     for B, S in ((0, 4), (2, 0)):
