@@ -599,40 +599,54 @@ __global__ void __launch_bounds__(256) k_attend_join(const AttendParams p, int c
   // a grid that ends before the one it depends on would let the next kernel of the
   // stream start early, so every warp waits
   pdl_wait();
+  // the running maximum and sums, U pieces at a time with all their loads in flight (one
+  // after the other they took 3 us here, most of it latency)
+  constexpr int U = 4;
   float M = -INFINITY, l = 0.f, l_r = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  if (joined) {
-    // c0's piece is its run's last, unless the run starts there
-    auto part_of = [&](uint32_t c) {
-      const int slot = runs.start(c) >= a ? 0 : 1;
-      return (static_cast<int64_t>(c) * 2 + slot) * (kTile * NX) + row_part;
-    };
-    for (uint32_t c = c0 + lane; c <= c1; c += 32)
-      if (has(c)) M = fmaxf(M, p.part_ml[part_of(c)].x);
+  auto scale = [&](float f) {
+    l *= f;
+    l_r *= f;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    const float Mu = M == -INFINITY ? 0.f : M;
+    for (int e = 0; e < E; ++e) o[e] *= f;
+  };
+  if (joined) {
     const uint32_t n = c1 - c0 + 1, z = c0 + n * (sub + 1) / WARPS;
-#pragma unroll 4
-    for (uint32_t c = c0 + n * sub / WARPS; c < z; ++c) {
-      if (!has(c)) continue;
-      const int64_t part = part_of(c);
-      const float4 ml = p.part_ml[part];
-      const float f = exp2f(ml.x - Mu);
-      l = fmaf(f, ml.y, l);
-      l_r = fmaf(f, ml.z, l_r);
-      const float *src = p.part_o + part * D + lane * E;
-      if constexpr (E == 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(src);
-        o[0] = fmaf(f, v.x, o[0]);
-        o[1] = fmaf(f, v.y, o[1]);
-        o[2] = fmaf(f, v.z, o[2]);
-        o[3] = fmaf(f, v.w, o[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2 *>(src);
-        o[0] = fmaf(f, v.x, o[0]);
-        o[1] = fmaf(f, v.y, o[1]);
+#pragma unroll 1
+    for (uint32_t c = c0 + n * sub / WARPS; c < z; c += U) {
+      float4 ml[U];
+      float v[U][E];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t cu = min(c + u, z - 1);
+        // c0's piece is its run's last, unless the run starts there
+        const int slot = runs.start(cu) >= a ? 0 : 1;
+        const int64_t part = (static_cast<int64_t>(cu) * 2 + slot) * (kTile * NX) + row_part;
+        ml[u] = p.part_ml[part];
+        const float *src = p.part_o + part * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) *reinterpret_cast<float2 *>(&v[u][e]) = *reinterpret_cast<const float2 *>(src + e);
+      }
+      const float before = M;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (c + u >= z || !has(c + u)) {  // what is there is no piece of this call
+          ml[u] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[u][e] = 0.f;
+        }
+        M = fmaxf(M, ml[u].x);
+      }
+      const float Mu = M == -INFINITY ? 0.f : M;
+      scale(exp2f(before - Mu));
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float f = exp2f(ml[u].x - Mu);
+        l = fmaf(f, ml[u].y, l);
+        l_r = fmaf(f, ml[u].z, l_r);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(f, v[u][e], o[e]);
       }
     }
   }
@@ -642,14 +656,22 @@ __global__ void __launch_bounds__(256) k_attend_join(const AttendParams p, int c
     if (lane == 0) {
       part_sm[warp][D] = l;
       part_sm[warp][D + 1] = l_r;
+      part_sm[warp][D + 2] = M;
     }
     __syncthreads();
     if (sub != 0) return;
-    for (int x = 1; x < WARPS; ++x) {
+    const float mine = M;
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += part_sm[warp + x][lane * E + e];
-      l += part_sm[warp + x][D];
-      l_r += part_sm[warp + x][D + 1];
+    for (int x = 1; x < WARPS; ++x) M = fmaxf(M, part_sm[warp + x][D + 2]);
+    const float Mu = M == -INFINITY ? 0.f : M;
+    scale(exp2f(mine - Mu));
+#pragma unroll
+    for (int x = 1; x < WARPS; ++x) {
+      const float f = exp2f(part_sm[warp + x][D + 2] - Mu);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(f, part_sm[warp + x][lane * E + e], o[e]);
+      l = fmaf(f, part_sm[warp + x][D], l);
+      l_r = fmaf(f, part_sm[warp + x][D + 1], l_r);
     }
   }
   if (!in || !(joined || padding)) return;
