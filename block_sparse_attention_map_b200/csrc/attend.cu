@@ -468,33 +468,33 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
         const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + w.slot) * (kTile * NX) +
                              (turns ? 0 : x * kTile) + r;
         float *prow = p.part_o + part * D;
-        // the columns [c0, c1) * 16: half of them where both groups hold a part of the row
-        const int c0 = both ? x * (D / 32) : 0, c1 = both ? c0 + D / 32 : D / 16;
-#pragma unroll 2
+        // the columns [c0, c1) * 32: half of them where both groups hold a part of the row
+        const int c0 = both ? x * (D / 64) : 0, c1 = both ? c0 + D / 64 : D / 32;
+#pragma unroll 1
         for (int c = c0; c < c1; ++c) {
-          uint32_t o[16];
-          tmem_ld16(t_o + c * 16, o);
+          uint32_t o[32];
+          tmem_ld32(t_o + c * 32, o);
           if (both) {
-            uint32_t o2[16];
-            tmem_ld16(tmem + lane_off + 256 + (x ^ 1) * D + c * 16, o2);
+            uint32_t o2[32];
+            tmem_ld32(tmem + lane_off + 256 + (x ^ 1) * D + c * 32, o2);
             tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
+            for (int q = 0; q < 32; ++q)
               o[q] = __float_as_uint(__uint_as_float(o[q]) * f_mine + __uint_as_float(o2[q]) * f_other);
           } else {
             tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f_mine);
+            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f_mine);
           }
           if (any_bad) {
-            // the seen tokens' infinities and NaN, in this row's 16 columns
+            // the seen tokens' infinities and NaN, in this row's 32 columns
             for (uint64_t todo = bad_lo | static_cast<uint64_t>(bad_hi) << 32; todo != 0ull; todo &= todo - 1) {
               const int s = w.s.len + __ffsll(static_cast<long long>(todo)) - 1, page = page_of(p.cache, w.b, s);
               if (page < 0) continue;
               const uint32_t *src = reinterpret_cast<const uint32_t *>(
-                  p.cache.v + slot_offset(p.cache.vs, p.cache, page, s, w.hk) + c * 16);
+                  p.cache.v + slot_offset(p.cache.vs, p.cache, page, s, w.hk) + c * 32);
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
+              for (int q = 0; q < 16; ++q) {
                 const uint32_t v = src[q], nf = not_finite<FP16>(v);
                 const float2 f = unpack16<FP16>(v);
                 if (nf & 0xffffu) o[2 * q] = __float_as_uint(__uint_as_float(o[2 * q]) + f.x);
@@ -504,19 +504,17 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
             __syncwarp();
           }
           if (row_ok) {
-            if (w.whole) {
-              uint32_t wv[8];
 #pragma unroll
-              for (int q = 0; q < 8; ++q)
-                wv[q] = pack16<FP16>(__uint_as_float(o[2 * q]), __uint_as_float(o[2 * q + 1]));
-              int4 *dst = reinterpret_cast<int4 *>(orow + c * 16);
-              dst[0] = make_int4(wv[0], wv[1], wv[2], wv[3]);
-              dst[1] = make_int4(wv[4], wv[5], wv[6], wv[7]);
-            } else {
-              const uint32_t(&lo)[8] = *reinterpret_cast<const uint32_t(*)[8]>(o);
-              const uint32_t(&hi)[8] = *reinterpret_cast<const uint32_t(*)[8]>(o + 8);
-              st_global_v8(prow + c * 16, lo);
-              st_global_v8(prow + c * 16 + 8, hi);
+            for (int k = 0; k < 4; ++k) {
+              if (w.whole) {
+                uint32_t wv[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  wv[q] = pack16<FP16>(__uint_as_float(o[8 * k + 2 * q]), __uint_as_float(o[8 * k + 2 * q + 1]));
+                reinterpret_cast<int4 *>(orow + c * 32)[k] = make_int4(wv[0], wv[1], wv[2], wv[3]);
+              } else {
+                st_global_v8(prow + c * 32 + 8 * k, *reinterpret_cast<const uint32_t(*)[8]>(&o[8 * k]));
+              }
             }
           }
           __syncwarp();
