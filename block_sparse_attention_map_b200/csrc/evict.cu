@@ -8,7 +8,7 @@
 // i-th into the i-th.  Sources lie at or past the budget and destinations below
 // it, so the moves need no order among themselves and touch only what changes.
 //
-// k_evict_select: a cluster of up to 8 CTAs per head, each with an equal share of
+// k_evict_select: a cluster of up to 16 CTAs per head, each with an equal share of
 // the head's slots in slot order and their keys in shared memory.  Four 8-bit
 // histogram passes (the CTAs' histograms summed over distributed shared memory)
 // find the key at the budget; two ordered counts over warps and CTAs then number
@@ -72,16 +72,18 @@ __device__ __forceinline__ int2 count_warps(int2 (&warp_n)[kSelWarps + 1], int2 
 // The moves [0, m) of a head, by the part-th of `parts` blocks: a group of D/8
 // lanes moves one slot's K and V, the block's moves of a step next to each other
 // (rows of one DRAM page: 74 us against 50 for 16 heads of 65536 slots with the
-// groups' moves apart).
+// groups' moves apart).  AHEAD: the next step's slots and pages are looked up while
+// this one's rows are in flight (the same 16 heads: 93 -> 84 us for the whole call).
+template <bool AHEAD>
 __device__ __forceinline__ void move_rows(const EvictArgs &a, int head, int m, int part, int parts) {
   constexpr int U = 2;  // moves of a group in flight
   const int b = head / a.cache.H_kv, hk = head % a.cache.H_kv;
   const int lanes = a.cache.D >> 3, moves = blockDim.x / lanes;
   const int sub = threadIdx.x % lanes, grp = threadIdx.x / lanes;
   const int64_t lb = static_cast<int64_t>(head) * a.list_cap, base = static_cast<int64_t>(head) * a.cache.capacity;
-  for (int i0 = part * U * moves + grp; i0 < m; i0 += parts * U * moves) {
-    int to[U], from[U], pt[U], pf[U];
-    int4 kv[U], vv[U];
+  int to[U], from[U], pt[U], pf[U];
+  // slots and pages of the moves i0, i0 + moves, ...
+  auto look = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * moves;
@@ -93,33 +95,58 @@ __device__ __forceinline__ void move_rows(const EvictArgs &a, int head, int m, i
       pt[u] = to[u] >= 0 ? page_of(a.cache, b, to[u]) : -1;
       pf[u] = to[u] >= 0 ? page_of(a.cache, b, from[u]) : -1;
     }
+  };
+  const int first = part * U * moves + grp, step = parts * U * moves;
+  if (AHEAD && first < m) look(first);
+  for (int i0 = first; i0 < m; i0 += step) {
+    if (!AHEAD) look(i0);
+    int4 kv[U], vv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (pt[u] < 0 || pf[u] < 0) continue;
       kv[u] = *reinterpret_cast<const int4 *>(a.cache.k + slot_offset(a.cache.ks, a.cache, pf[u], from[u], hk) + sub * 8);
       vv[u] = *reinterpret_cast<const int4 *>(a.cache.v + slot_offset(a.cache.vs, a.cache, pf[u], from[u], hk) + sub * 8);
     }
+    int now[U];
+    bool good[U];
+    float sc[U];
+    int ps[U];
+    uint16_t *kd[U], *vd[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (to[u] < 0) continue;
-      if (pt[u] >= 0 && pf[u] >= 0) {
-        *reinterpret_cast<int4 *>(a.cache.k + slot_offset(a.cache.ks, a.cache, pt[u], to[u], hk) + sub * 8) = kv[u];
-        *reinterpret_cast<int4 *>(a.cache.v + slot_offset(a.cache.vs, a.cache, pt[u], to[u], hk) + sub * 8) = vv[u];
+      now[u] = to[u];
+      good[u] = pt[u] >= 0 && pf[u] >= 0;
+      if (good[u]) {
+        kd[u] = a.cache.k + slot_offset(a.cache.ks, a.cache, pt[u], to[u], hk) + sub * 8;
+        vd[u] = a.cache.v + slot_offset(a.cache.vs, a.cache, pt[u], to[u], hk) + sub * 8;
+      }
+      if (sub == 0 && to[u] >= 0) {
+        sc[u] = a.mscore[lb + i0 + u * moves];
+        ps[u] = a.mpos[lb + i0 + u * moves];
+      }
+    }
+    if (AHEAD && i0 + step < m) look(i0 + step);  // under the rows' loads
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (now[u] < 0) continue;
+      if (good[u]) {
+        *reinterpret_cast<int4 *>(kd[u]) = kv[u];
+        *reinterpret_cast<int4 *>(vd[u]) = vv[u];
       } else if (sub == 0) {
         record_status(a.cache.status, BSA_ERR_BAD_CACHE);
       }
       if (sub == 0) {
-        a.score_out[base + to[u]] = a.mscore[lb + i0 + u * moves];
-        a.pos_out[base + to[u]] = a.mpos[lb + i0 + u * moves];
+        a.score_out[base + now[u]] = sc[u];
+        a.pos_out[base + now[u]] = ps[u];
       }
     }
   }
 }
 
-// K > 0: a thread's keys in K registers; K = 0: in shared memory where key_cap
+// CLUSTER: a head has several CTAs.  K > 0: a thread's keys in K registers; K = 0: in shared memory where key_cap
 // holds them, else read again by each pass.  MOVES: the CTAs move their head's rows
 // too (and where the lengths do not change in place, write them).
-template <int kSelThreads, int K, bool MOVES>
+template <int kSelThreads, int K, bool CLUSTER, bool MOVES>
 __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) k_evict_select(const EvictArgs a, int key_cap) {
   constexpr int kSelWarps = kSelThreads / 32;
   extern __shared__ uint32_t keys[];  // [key_cap]: this CTA's, where they fit
@@ -127,7 +154,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) k_evict_selec
   __shared__ uint32_t sel[3];         // chosen digit, what is still wanted within it, the keys of it in lower CTAs
   __shared__ int2 counts[2][kSelWarps + 1];
   cg::cluster_group cluster = cg::this_cluster();
-  const unsigned ctas = cluster.num_blocks(), rank = cluster.block_rank();
+  const unsigned ctas = CLUSTER ? cluster.num_blocks() : 1u, rank = CLUSTER ? cluster.block_rank() : 0u;
   const int head = blockIdx.x / ctas, b = head / a.cache.H_kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t base = static_cast<int64_t>(head) * a.cache.capacity;
@@ -170,6 +197,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) k_evict_selec
       for (int i0 = w0; i0 < w1; i0 += 32) f(0, i0 + lane);
     }
   };
+  static_assert(K == 0 || K == 8, "a cluster's last pass takes a lane's slots eight at a time");
   auto key = [&](int k, int i) {
     if constexpr (K > 0) return regs[k];
     else return i >= w1 ? 0u : kept_here ? keys[i - s0] : key_of(i);
@@ -215,7 +243,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) k_evict_selec
       const uint32_t x = key(k, i);
       if (i < w1 && (x & mask) == prefix) atomicAdd(&mine[(x >> shift) & 255u], 1u);
     });
-    if (ctas > 1) cluster.sync();
+    if (CLUSTER) cluster.sync();
     else __syncthreads();
     if (warp == 0) {
       // lane l: the digits 255 - 8 l down to 248 - 8 l
@@ -225,7 +253,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) k_evict_selec
       uint32_t low[8];  // of the CTAs before this one
 #pragma unroll
       for (int k = 0; k < 8; ++k) low[k] = 0;
-      if (ctas == 1) {
+      if (!CLUSTER) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = mine[255 - 8 * lane - k];
       } else {
@@ -303,7 +331,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) k_evict_selec
   movers += tie_keep - low_keep;
   const int2 in_cta = count_warps<kSelWarps>(counts[1], make_int2(holes, movers));
   int hole_at = in_cta.x, mover_at = in_cta.y, moved = counts[1][kSelWarps].y;
-  if (ctas > 1) {
+  if (CLUSTER) {
     cluster.sync();
     // every lane one CTA's totals, added up over the warp
     const int2 t = lane < static_cast<int>(ctas) ? cluster.map_shared_rank(&counts[1][kSelWarps], lane)[0] : make_int2(0, 0);
@@ -320,9 +348,8 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) k_evict_selec
   // the outputs are the inputs.
   const bool copies = score_out != score || pos_out != pos;
   int seen = ties_before;
-  each([&](int kk, int i) {
+  auto place = [&](uint32_t x, int i, auto get) {
     const bool in = i < w1;
-    const uint32_t x = key(kk, i);
     const uint32_t tb = __ballot_sync(0xffffffffu, in && x == prefix);
     const bool k = in && (x > prefix || (x == prefix && seen + __popc(tb & below) < static_cast<int>(want)));
     seen += __popc(tb);
@@ -333,8 +360,9 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) k_evict_selec
     if (hole && ha < a.list_cap) to[ha] = i;
     const bool copy = k && copies && i < a.budget;  // (holes are filled by the move)
     if (mover || copy) {
-      const float sc = score[i];
-      const int ps = pos[i];
+      float sc;
+      int ps;
+      get(sc, ps);
       if (copy) {
         score_out[i] = sc;
         pos_out[i] = ps;
@@ -350,19 +378,54 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) k_evict_selec
     }
     hole_at += __popc(hb);
     mover_at += __popc(mb);
-  });
+  };
+  if constexpr (CLUSTER) {
+    // all of what may move or be copied, eight slots of a lane in flight (65536 slots to half: 38 -> 34 us; a CTA alone
+    // has too many threads for the registers, 11.6 -> 12.5 us for 4097 slots)
+    constexpr int U = 8;
+    for (int i0 = w0; i0 < w1; i0 += 32 * U) {
+      float sc[U];
+      int ps[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + 32 * u + lane;
+        sc[u] = 0.f;
+        ps[u] = 0;
+        if (i < w1 && (copies || i >= a.budget)) {
+          sc[u] = score[i];
+          ps[u] = pos[i];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + 32 * u + lane;
+        if (i0 + 32 * u < w1)
+          place(key(u, i), i, [&](float &x, int &y) {
+            x = sc[u];
+            y = ps[u];
+          });
+      }
+    }
+  } else {
+    each([&](int k, int i) {
+      place(key(k, i), i, [&](float &x, int &y) {
+        x = score[i];
+        y = pos[i];
+      });
+    });
+  }
   if (!MOVES && tid == 0 && rank == 0) a.count[head] = min(moved, a.list_cap);
   // no CTA leaves while another may read its shared memory; and the lists are whole
-  if (ctas > 1) cluster.sync();
+  if (CLUSTER) cluster.sync();
   else __syncthreads();
-  if (MOVES) move_rows(a, head, min(moved, a.list_cap), rank, ctas);
+  if (MOVES) move_rows<false>(a, head, min(moved, a.list_cap), rank, ctas);
 }
 
 // The moves by every SM, and the new lengths (the selection is done with the old ones).
 __global__ void __launch_bounds__(256) k_evict_move(const EvictArgs a, int per_head) {
   const int head = blockIdx.x / per_head, part = blockIdx.x % per_head;
   pdl_wait();
-  move_rows(a, head, a.count[head], part, per_head);
+  move_rows<true>(a, head, a.count[head], part, per_head);
   if (part == 0 && head % a.cache.H_kv == 0 && threadIdx.x == 0) {
     const int b = head / a.cache.H_kv;
     a.length_out[b] = min(min(max(a.cache.length[b], 0), a.cache.capacity), a.budget);
@@ -376,10 +439,10 @@ __global__ void __launch_bounds__(256) k_evict_length(const EvictArgs a) {
   if (b < a.cache.B) a.length_out[b] = min(min(max(a.cache.length[b], 0), a.cache.capacity), a.budget);
 }
 
-template <int THREADS, int K, bool MOVES>
+template <int THREADS, int K, bool CLUSTER, bool MOVES>
 cudaError_t select(const EvictArgs &a, int heads, int ctas, cudaStream_t s) {
   constexpr int kWarps = THREADS / 32;
-  const auto kernel = k_evict_select<THREADS, K, MOVES>;
+  const auto kernel = k_evict_select<THREADS, K, CLUSTER, MOVES>;
   // a CTA's slots, at most
   const int share = ((a.cache.capacity + 31) / 32 + ctas * kWarps - 1) / (ctas * kWarps) * THREADS;
   const int key_cap = K == 0 && share <= kMaxKeys ? share : 0;
@@ -406,19 +469,19 @@ cudaError_t select(const EvictArgs &a, int heads, int ctas, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kernel, a, key_cap);
 }
 
-template <int THREADS, int K>
+template <int THREADS, int K, bool CLUSTER>
 cudaError_t evict(const EvictArgs &a, int ctas, cudaStream_t s) {
   const int heads = a.cache.B * a.cache.H_kv;
   // The CTAs that select move the rows too where no more than a few can move (one
   // launch less: 4097 slots to 4096 13.2 -> 11.6 us); else a second kernel on all SMs
   // (32 heads of 32768 slots to half by the selecting CTAs: 107 us against 87).
   if (a.list_cap <= 512) {
-    const cudaError_t e = select<THREADS, K, true>(a, heads, ctas, s);
+    const cudaError_t e = select<THREADS, K, CLUSTER, true>(a, heads, ctas, s);
     if (e != cudaSuccess || a.length_out != a.cache.length) return e;
     count_launch();
     return launch_pdl(k_evict_length, dim3((a.cache.B + 255) / 256), dim3(256), 0, s, a);
   }
-  const cudaError_t e = select<THREADS, K, false>(a, heads, ctas, s);
+  const cudaError_t e = select<THREADS, K, CLUSTER, false>(a, heads, ctas, s);
   if (e != cudaSuccess) return e;
   const int per_head = std::max(1, std::min((148 * 8 + heads - 1) / heads, (a.list_cap + 15) / 16));
   count_launch();
@@ -433,15 +496,15 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s) {
   // a cluster of CTAs of 512 threads, so that an SM holds two (16 clusters of 8 x
   // 1024 did not fit the GPU at once: 85 us against 37 for the selection of 65536).
   const int cap = a.cache.capacity;
-  if (cap <= 2048) return evict<256, 8>(a, 1, s);
-  if (cap <= 4096) return evict<512, 8>(a, 1, s);
-  if (cap <= 8192) return evict<1024, 8>(a, 1, s);
-  if (cap <= 16384) return evict<512, 8>(a, 4, s);
-  if (cap <= 32768) return evict<512, 8>(a, 8, s);
+  if (cap <= 2048) return evict<256, 8, false>(a, 1, s);
+  if (cap <= 4096) return evict<512, 8, false>(a, 1, s);
+  if (cap <= 8192) return evict<1024, 8, false>(a, 1, s);
+  if (cap <= 16384) return evict<512, 8, true>(a, 4, s);
+  if (cap <= 32768) return evict<512, 8, true>(a, 8, s);
   // 16 CTAs where the heads are few (1 head of 10^6 slots 836 -> 459 us; 16 heads of
   // 65536 found too few places for such clusters: 94 -> 168 us)
-  if (a.cache.B * a.cache.H_kv <= 4) return cap <= 65536 ? evict<512, 8>(a, 16, s) : evict<512, 0>(a, 16, s);
-  return evict<512, 0>(a, 8, s);
+  if (a.cache.B * a.cache.H_kv <= 4) return cap <= 65536 ? evict<512, 8, true>(a, 16, s) : evict<512, 0, true>(a, 16, s);
+  return evict<512, 0, true>(a, 8, s);
 }
 
 }  // namespace bsa
