@@ -12,7 +12,7 @@
 // Bound: HBM; the only reads besides the tensors are the positions and the two
 // small tables.  (A thread that computed its own chunk's sines for each share of
 // the heads spent more time on them than on the rows where heads are few: 8192
-// tokens x 20 heads 30 us, now 17.)
+// tokens x 20 heads 30 us, now 16.)
 //
 // The angle is reduced before any rounding to 32 bits: the frequency in turns
 // is a 64-bit fraction of a turn, so its product with the integer position
@@ -65,7 +65,7 @@ __device__ __forceinline__ int4 turn_interleaved(int4 v, const float *c, const f
   return make_int4(w[0], w[1], w[2], w[3]);
 }
 
-template <bool FP16>
+template <bool FP16, bool APPEND>
 __device__ __forceinline__ void turn_halves(int4 &v0, int4 &v1, const float (&c)[8], const float (&s)[8],
                                             uint32_t rot) {
   uint32_t x[4] = {static_cast<uint32_t>(v0.x), static_cast<uint32_t>(v0.y), static_cast<uint32_t>(v0.z),
@@ -77,6 +77,11 @@ __device__ __forceinline__ void turn_halves(int4 &v0, int4 &v1, const float (&c)
     const float2 a = unpack16<FP16>(x[i]), b = unpack16<FP16>(y[i]);
     const uint32_t u = pack16<FP16>(a.x * c[2 * i] - b.x * s[2 * i], a.y * c[2 * i + 1] - b.y * s[2 * i + 1]);
     const uint32_t w = pack16<FP16>(a.x * s[2 * i] + b.x * c[2 * i], a.y * s[2 * i + 1] + b.y * c[2 * i + 1]);
+    if (!APPEND && rot == 0xffu) {
+      x[i] = u;
+      y[i] = w;
+      continue;
+    }
     // a copied pair keeps its bits (0 * infinity would make it NaN)
     const uint32_t m = ((rot >> (2 * i)) & 1u ? 0xffffu : 0u) | ((rot >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
     x[i] = (u & m) | (x[i] & ~m);
@@ -91,7 +96,10 @@ struct RopeGrid {
   int pairs;                             // whose sines are computed (0: k and v as they are)
 };
 
-template <bool FP16, bool HALVES>
+// APPEND: k and v go into the cache's slots.  (One kernel for both had no registers
+// left in the other case: 75600 tokens x 80 heads in halves 507 us, now 490, 8192 x
+// 20 heads 17.4 and 16.4.)
+template <bool FP16, bool HALVES, bool APPEND>
 __global__ void __launch_bounds__(256, 4) k_rope(const RopeArgs a, const RopeGrid g) {
   constexpr int P = 8;  // pairs of a thread: one chunk of each half's, or two chunks of four
   constexpr int U = 2;  // heads in flight
@@ -130,7 +138,7 @@ __global__ void __launch_bounds__(256, 4) k_rope(const RopeArgs a, const RopeGri
     const uint16_t *k_src = a.k + b * a.ks[0] + t * a.ks[1] + e0, *v_src = nullptr;
     uint16_t *k_dst = a.ko + b * a.kos[0] + t * a.kos[1] + e0, *v_dst = nullptr;
     int n_heads = on ? g.n_heads : 0;
-    if (a.append && on) {
+    if (APPEND && on) {
       const bool report = c == 0 && h0 == 0;
       const int len = clamped_length(a.cache, b, report);
       const int n = clamped_new(a.cache, a.tok, b, len, report);
@@ -144,12 +152,12 @@ __global__ void __launch_bounds__(256, 4) k_rope(const RopeArgs a, const RopeGri
         if (report && t < n) record_status(a.cache.status, BSA_ERR_BAD_CACHE);
       }
     }
-    const int64_t k_ds = a.append ? a.cache.ks[2] : a.kos[2], v_ds = a.append ? a.cache.vs[2] : 0;
+    const int64_t k_ds = APPEND ? a.cache.ks[2] : a.kos[2], v_ds = APPEND ? a.cache.vs[2] : 0;
     auto src_of = [&](int i) {
-      return i < nq ? q_src + i * a.qs[2] : i < nq + a.H_kv ? k_src + (i - nq) * a.ks[2] : v_src + (i - nq - a.H_kv) * a.vs[2];
+      return i < nq ? q_src + i * a.qs[2] : !APPEND || i < nq + a.H_kv ? k_src + (i - nq) * a.ks[2] : v_src + (i - nq - a.H_kv) * a.vs[2];
     };
     auto dst_of = [&](int i) {
-      return i < nq ? q_dst + i * a.qos[2] : i < nq + a.H_kv ? k_dst + (i - nq) * k_ds : v_dst + (i - nq - a.H_kv) * v_ds;
+      return i < nq ? q_dst + i * a.qos[2] : !APPEND || i < nq + a.H_kv ? k_dst + (i - nq) * k_ds : v_dst + (i - nq - a.H_kv) * v_ds;
     };
     int4 v0[U], v1[U];
     auto load = [&](int h) {
@@ -196,9 +204,9 @@ __global__ void __launch_bounds__(256, 4) k_rope(const RopeArgs a, const RopeGri
       for (int u = 0; u < U; ++u) {
         const int i = h + u * g.lanes;
         if (i >= n_heads) continue;
-        if (rot != 0u && i < nq + a.H_kv) {
+        if (rot != 0u && (!APPEND || i < nq + a.H_kv)) {
           if constexpr (HALVES) {
-            turn_halves<FP16>(v0[u], v1[u], cs, sn, rot);
+            turn_halves<FP16, APPEND>(v0[u], v1[u], cs, sn, rot);
           } else {
             v0[u] = turn_interleaved<FP16>(v0[u], cs, sn, rot);
             v1[u] = turn_interleaved<FP16>(v1[u], cs + 4, sn + 4, rot >> 4);
@@ -212,10 +220,10 @@ __global__ void __launch_bounds__(256, 4) k_rope(const RopeArgs a, const RopeGri
   }
 }
 
-template <bool FP16, bool HALVES>
+template <bool FP16, bool HALVES, bool APPEND>
 cudaError_t launch(const RopeArgs &a, cudaStream_t s) {
   RopeGrid g;
-  g.n_heads = (a.q != nullptr ? a.H : 0) + (a.append ? 2 * a.H_kv : a.k != nullptr ? a.H_kv : 0);
+  g.n_heads = (a.q != nullptr ? a.H : 0) + (APPEND ? 2 * a.H_kv : a.k != nullptr ? a.H_kv : 0);
   g.n_chunks = HALVES ? a.D / 8 - a.n_pairs / 8 : a.D / 16;
   g.pairs = !a.rotate ? 0 : HALVES ? a.n_pairs : a.D / 2;
   const int64_t rows = static_cast<int64_t>(a.B) * a.T;
@@ -228,14 +236,18 @@ cudaError_t launch(const RopeArgs &a, cudaStream_t s) {
   g.lanes = std::max(1, std::min(shares / g.tokens, g.n_heads));
   const int64_t blocks = std::min<int64_t>((rows + g.tokens - 1) / g.tokens, 148 * 8);
   count_launch();
-  return launch_pdl(k_rope<FP16, HALVES>, dim3(static_cast<unsigned>(blocks)), dim3(256), (g.tokens * 16 + 1) * g.pairs, s, a, g);
+  return launch_pdl(k_rope<FP16, HALVES, APPEND>, dim3(static_cast<unsigned>(blocks)), dim3(256), (g.tokens * 16 + 1) * g.pairs, s, a, g);
 }
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeArgs &a, bool halves, bool fp16, cudaStream_t s) {
-  if (fp16) return halves ? launch<true, true>(a, s) : launch<true, false>(a, s);
-  return halves ? launch<false, true>(a, s) : launch<false, false>(a, s);
+cudaError_t launch_rope(const RopeArgs &a, bool halves, bool fp16, bool append, cudaStream_t s) {
+  if (append) {
+    if (fp16) return halves ? launch<true, true, true>(a, s) : launch<true, false, true>(a, s);
+    return halves ? launch<false, true, true>(a, s) : launch<false, false, true>(a, s);
+  }
+  if (fp16) return halves ? launch<true, true, false>(a, s) : launch<true, false, false>(a, s);
+  return halves ? launch<false, true, false>(a, s) : launch<false, false, false>(a, s);
 }
 
 }  // namespace bsa

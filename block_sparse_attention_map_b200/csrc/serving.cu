@@ -233,7 +233,7 @@ bsa_status bsa_rope(const bsa_tokens *tok, const bsa_rope_spec *rope, const void
   copy3(a.ks, t.ks);
   copy3(a.qos, t.qos);
   copy3(a.kos, t.kos);
-  return of_cuda(launch_rope(a, rope->layout == BSA_ROPE_HALVES, t.t.dtype == BSA_DTYPE_FP16,
+  return of_cuda(launch_rope(a, rope->layout == BSA_ROPE_HALVES, t.t.dtype == BSA_DTYPE_FP16, false,
                              reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -277,10 +277,9 @@ bsa_status bsa_cache_append(const bsa_cache *cache, const bsa_tokens *tok, const
   copy3(a.ks, t.ks);
   copy3(a.vs, t.vs);
   copy3(a.qos, t.qos);
-  a.append = 1;
   a.cache = c;
   a.tok = token_view(t.t);
-  return of_cuda(launch_rope(a, rope != nullptr && rope->layout == BSA_ROPE_HALVES, t.t.dtype == BSA_DTYPE_FP16,
+  return of_cuda(launch_rope(a, rope != nullptr && rope->layout == BSA_ROPE_HALVES, t.t.dtype == BSA_DTYPE_FP16, true,
                              reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -107,11 +107,10 @@ struct RopeArgs {
   const uint16_t *q, *k, *v;
   uint16_t *qo, *ko;
   int64_t qs[3], ks[3], vs[3], qos[3], kos[3];
-  int append;        // k and v go into the cache's slots
-  CacheView cache;
+  CacheView cache;   // append: k and v go into its slots
   TokenView tok;
 };
-cudaError_t launch_rope(const RopeArgs &a, bool halves, bool fp16, cudaStream_t s);
+cudaError_t launch_rope(const RopeArgs &a, bool halves, bool fp16, bool append, cudaStream_t s);
 
 struct AttendArgs {
   CacheView cache;
