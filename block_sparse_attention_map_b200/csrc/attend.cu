@@ -28,9 +28,9 @@
 //               heads a group over 33002 keys; key tiles taken as two halves, to
 //               overlap more, spent more on the barriers: 182 against 148 us at
 //               24000 keys).
-// V of what no row may see: slots past the new tokens are zeroed in shared memory
-// (0 * NaN is NaN in the product), and a new token's infinities and NaN are taken
-// out of the tile and added back in the epilogue of the rows that see the token.
+// V of what no row may see (0 * NaN is NaN in the product): infinities and NaN past
+// the new tokens are taken out of the tile in shared memory, and so are those of a
+// new token, which the epilogue of the rows that see the token adds back.
 // TMEM columns: S_0 [0,128) S_1 [128,256) O_0 [256,256+D) O_1 [256+D,256+2D).
 #include "runs.cuh"
 
@@ -324,10 +324,9 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
         tc_fence_after();
         // After S: the products of the tiles that had this V stage before are done (they were issued before S), so
         // the stage's phase is this tile's.  (Waited for before S, it could still be at the tile before in the stage,
-        // whose V this would have zeroed.)
+        // whose V this would have changed.)
         if (edge && (turns || x == 0)) {
-          // this thread's key: V past the new tokens becomes zero, what is not
-          // finite in a new token's V is taken out
+          // this thread's key: what is not finite in V of a new token, or past them, is taken out
           if (!wwait(&bars[L::bVFull + kv % NV], (kv / NV) & 1)) { stop = true; break; }
           uint8_t *vrow = sm + L::kV + (kv % NV) * kTB + r * 128;
           const int d = j0 + r - w.s.len;
@@ -336,19 +335,17 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
 #pragma unroll 8
             for (int c = 0; c < kPieces; ++c) {
               int4 *q4 = reinterpret_cast<int4 *>(vrow + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4));
-              int4 v = make_int4(0, 0, 0, 0);
-              if (d < w.s.n) {
-                v = *q4;
-                const uint32_t n0 = not_finite<FP16>(v.x), n1 = not_finite<FP16>(v.y), n2 = not_finite<FP16>(v.z),
-                               n3 = not_finite<FP16>(v.w);
-                if ((n0 | n1 | n2 | n3) == 0u) continue;
-                found = true;
-                v = make_int4(v.x & ~n0, v.y & ~n1, v.z & ~n2, v.w & ~n3);
-              }
-              *q4 = v;
+              const int4 v = *q4;
+              const uint32_t n0 = not_finite<FP16>(v.x), n1 = not_finite<FP16>(v.y), n2 = not_finite<FP16>(v.z),
+                             n3 = not_finite<FP16>(v.w);
+              if ((n0 | n1 | n2 | n3) == 0u) continue;
+              found = true;
+              *q4 = make_int4(v.x & ~n0, v.y & ~n1, v.z & ~n2, v.w & ~n3);
             }
-            if (found) atomicOr(bad_w + (d >> 5), 1u << (d & 31));
-            fence_proxy_async_smem();
+            if (found) {
+              if (d < w.s.n) atomicOr(bad_w + (d >> 5), 1u << (d & 31));
+              fence_proxy_async_smem();
+            }
           }
           __syncwarp();
         }
