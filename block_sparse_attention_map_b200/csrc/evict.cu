@@ -502,8 +502,10 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s) {
   if (cap <= 16384) return evict<512, 8, true>(a, 4, s);
   if (cap <= 32768) return evict<512, 8, true>(a, 8, s);
   // 16 CTAs where the heads are few (1 head of 10^6 slots 836 -> 459 us; 16 heads of
-  // 65536 found too few places for such clusters: 94 -> 168 us)
-  if (a.cache.B * a.cache.H_kv <= 4) return cap <= 65536 ? evict<512, 8, true>(a, 16, s) : evict<512, 0, true>(a, 16, s);
+  // 65536 found too few places for such clusters: 94 -> 168 us), and where the keys
+  // of a head do not fit the shared memory of 8 (16 heads of 500000 444 -> 227 us)
+  if (cap <= 65536 && a.cache.B * a.cache.H_kv <= 4) return evict<512, 8, true>(a, 16, s);
+  if (cap > 8 * kMaxKeys || a.cache.B * a.cache.H_kv <= 4) return evict<512, 0, true>(a, 16, s);
   return evict<512, 0, true>(a, 8, s);
 }
 

@@ -391,7 +391,8 @@ def test_evict_matches_oracle(lengths, H_kv, page, dtype, D, budget, sinks, rece
 
 @pytest.mark.parametrize("keys,H_kv,D,budget", [
     (2000, 3, 64, 1700), (4000, 2, 64, 3999), (8000, 2, 128, 100), (12000, 2, 64, 6000), (30000, 2, 64, 17001),
-    (50000, 5, 64, 20000), (50000, 3, 64, 49990), (150000, 1, 64, 70000), (900000, 1, 64, 400000)])
+    (50000, 5, 64, 20000), (50000, 3, 64, 49990), (150000, 1, 64, 70000), (900000, 1, 64, 400000),
+    (30000, 2, 64, 29900), (50000, 1, 64, 49900), (90000, 3, 64, 30000), (90000, 3, 64, 300), (400000, 5, 64, 1000)])
 def test_evict_of_every_size(keys, H_kv, D, budget):
     """One call of each way the selection is laid out (slots a CTA, cluster sizes, keys
     in registers, in shared memory and read again), against a stable sort."""
