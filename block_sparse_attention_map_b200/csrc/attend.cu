@@ -4,7 +4,9 @@
 //
 // The T * G rows of a kv head's group (row = t * G + g) share its keys, so K and
 // V are read once for up to 256 of them: one or two 128-row tiles (NX) against
-// 128-key tiles.  Up to about 200 rows the floor is HBM (4 D bytes a key).
+// 128-key tiles.  Up to about 200 rows the floor is HBM (4 D bytes a key): 6.4 TB/s
+// at 4 sequences x 1 token over 65536 keys, 5.6 at 16 x 32 tokens x 4 heads a group
+// over 33002 (151 us); 860 TFLOP/s at 256 rows.
 //
 // k_attend: one CTA per SM.  The (sequence, kv head, row group, key tile) list is
 // cut into equal runs, one a CTA, whatever the lengths are (they are read on the
@@ -41,7 +43,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Up to this capacity a CTA takes its rows' whole sequence, padding rows too, and
 // nothing is joined: four key tiles one after the other take less than a second
-// launch (2 heads, 7 tokens, 250 keys: 10.8 us with it).
+// launch (8 sequences x 1 token over 400 keys: 12.4 us with it, 11.4 without).
 constexpr int kWholeSlots = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: tolerate p up to 2^8
 

@@ -12,7 +12,7 @@
 // the head's slots in slot order and their keys in shared memory.  Four 8-bit
 // histogram passes (the CTAs' histograms summed over distributed shared memory)
 // find the key at the budget; two ordered counts over warps and CTAs then number
-// ties, holes and movers.  Bound: the latency of the passes, about 1 us each; one
+// ties, holes and movers.  Bound: the latency of the passes, about 1 us each (3.4 in a cluster); one
 // CTA a head took 337 us for 65536 slots and 49 us for 4097.
 // k_evict_move: a group of D/8 lanes moves one slot's K and V, 16 bytes a lane,
 // over all SMs.  Bound: HBM.
@@ -473,8 +473,8 @@ template <int THREADS, int K, bool CLUSTER>
 cudaError_t evict(const EvictArgs &a, int ctas, cudaStream_t s) {
   const int heads = a.cache.B * a.cache.H_kv;
   // The CTAs that select move the rows too where no more than a few can move (one
-  // launch less: 4097 slots to 4096 13.2 -> 11.6 us); else a second kernel on all SMs
-  // (32 heads of 32768 slots to half by the selecting CTAs: 107 us against 87).
+  // launch less: 4097 slots to 4096 13.3 -> 11.5 us); else a second kernel on all SMs
+  // (32 heads of 32768 slots to half by the selecting CTAs: 104 us against 75).
   if (a.list_cap <= 512) {
     const cudaError_t e = select<THREADS, K, CLUSTER, true>(a, heads, ctas, s);
     if (e != cudaSuccess || a.length_out != a.cache.length) return e;
@@ -494,15 +494,15 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s) {
   // A head's slots are 8 a thread of one CTA up to 8192 (few slots in a large CTA
   // are slots for no one: 512 heads of 1025 slots 39 us with 1024 threads), else of
   // a cluster of CTAs of 512 threads, so that an SM holds two (16 clusters of 8 x
-  // 1024 did not fit the GPU at once: 85 us against 37 for the selection of 65536).
+  // 1024 did not fit the GPU at once: over twice the time for the selection of 65536).
   const int cap = a.cache.capacity;
   if (cap <= 2048) return evict<256, 8, false>(a, 1, s);
   if (cap <= 4096) return evict<512, 8, false>(a, 1, s);
   if (cap <= 8192) return evict<1024, 8, false>(a, 1, s);
   if (cap <= 16384) return evict<512, 8, true>(a, 4, s);
   if (cap <= 32768) return evict<512, 8, true>(a, 8, s);
-  // 16 CTAs where the heads are few (1 head of 10^6 slots 836 -> 459 us; 16 heads of
-  // 65536 found too few places for such clusters: 94 -> 168 us), and where the keys
+  // 16 CTAs where the heads are few (1 head of 10^6 slots 806 -> 442 us; 16 heads of
+  // 65536 found too few places for such clusters: 83 -> 101 us), and where the keys
   // of a head do not fit the shared memory of 8 (16 heads of 500000 444 -> 227 us)
   if (cap <= 65536 && a.cache.B * a.cache.H_kv <= 4) return evict<512, 8, true>(a, 16, s);
   if (cap > 8 * kMaxKeys || a.cache.B * a.cache.H_kv <= 4) return evict<512, 0, true>(a, 16, s);

@@ -12,7 +12,7 @@
 // Bound: HBM; the only reads besides the tensors are the positions and the two
 // small tables.  (A thread that computed its own chunk's sines for each share of
 // the heads spent more time on them than on the rows where heads are few: 8192
-// tokens x 20 heads 30 us, now 16.)
+// tokens x 20 heads 30 us, now 17.)
 //
 // The angle is reduced before any rounding to 32 bits: the frequency in turns
 // is a 64-bit fraction of a turn, so its product with the integer position
@@ -228,7 +228,7 @@ cudaError_t launch(const RopeArgs &a, cudaStream_t s) {
   g.pairs = !a.rotate ? 0 : HALVES ? a.n_pairs : a.D / 2;
   const int64_t rows = static_cast<int64_t>(a.B) * a.T;
   // a thread takes about 20 heads (few waits for the sines a byte: 75600 tokens x
-  // 80 heads 508 us, with 8 heads 566) where there are tokens enough for four
+  // 80 heads 499 us, with 8 heads 539) where there are tokens enough for four
   // blocks an SM, else fewer tokens a block and fewer heads a thread
   const int shares = 256 / g.n_chunks;
   const int64_t few = (rows + 4 * 148 - 1) / (4 * 148);

@@ -12,12 +12,12 @@ namespace bsa {
 // all of them in order (b, kv head, row group, tile).  It is measured in units: a
 // key tile of a group with two row tiles is 3, of one with a single one 2 (4240
 // against about 2700 clocks measured; with equal shares of tiles 2 sequences x 64
-// tokens x 5 heads a group, rows 256 + 64, over 75600 keys took 341 us, now 306),
+// tokens x 5 heads a group, rows 256 + 64, over 75600 keys took 341 us, now 285),
 // where every group is alike 1; and each item begins with kSwitch units of no tile,
 // for what changing to it costs the run's CTA (the sums and O of the item before, the
 // pipeline's refill: the CTAs with an item's start among their tiles were last by 6
-// of 34 us at 8 sequences x 1 token over 8192 keys, 42 us in all without, 39 with;
-// 2048 keys 27 and 22).  With WHOLE, the list is of items instead, every
+// of 34 us at 8 sequences x 1 token over 8192 keys, 36.4 us in all without, 33.6
+// with; 2048 keys 20.9 and 18.0).  With WHOLE, the list is of items instead, every
 // row of the T * G in one, and a run takes each from its first tile to its last.
 constexpr int kAllRows = 0;
 

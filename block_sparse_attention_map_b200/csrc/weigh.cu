@@ -15,7 +15,7 @@
 //   warps 4-19  four groups, each with every fourth tile and a 128-column buffer
 //               of its own (two groups on 256 columns, reading 16 columns at a
 //               time, left the exponential unit idle two thirds of the time: 137
-//               us against 105 at 4 x 16 tokens x 5 heads a group, 75600 keys).
+//               us against 100 at 4 x 16 tokens x 5 heads a group, 75600 keys).
 // Up to 256 rows are in shared memory, as two halves that a batch of four tiles
 // takes one after the other; more rows walk the piece's tiles again, adding to
 // the same scores.
