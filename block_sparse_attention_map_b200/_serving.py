@@ -401,7 +401,6 @@ class PagedCache:
         self.workspace = CacheWorkspace(self.device) if workspace is None else workspace
         if self.workspace.device != self.device:
             raise ValueError("workspace: on another device")
-        self._reserved = 0  # the largest budget whose lists the workspace holds
         self.reserve(0)
 
     k = _held(0, "k")
@@ -415,7 +414,6 @@ class PagedCache:
         budget = _int32(budget, "budget")
         _check(_fn("bsa_cache_workspace_size")(self._c, budget, ctypes.byref(n)), "bsa_cache_workspace_size")
         self.workspace.grow(n.value)
-        self._reserved = max(self._reserved, budget)
 
     def _run(self, name, *args):
         """A library call on the cache, on the current stream."""
@@ -494,7 +492,8 @@ class PagedCache:
 
     def attend(self, q, tree=None, n_new=None, scale=None, out=None, lse=None):
         """(out, lse) of T <= 64 new tokens' queries [B, T, H, D] over the cache,
-        which already holds the new tokens' keys (:meth:`append`).  Token t sees
+        which already holds the new tokens' keys (:meth:`append`); out does not
+        overlap q.  Token t sees
         the slots below ``length`` and the new tokens of its word in ``tree``
         (int64 [B, T], :func:`tree_words`; None: a chain).  Rows at or past
         ``n_new`` are written as 0 / -inf."""
@@ -559,9 +558,13 @@ class PagedCache:
                 _check_flat(self._c.length, e.length_out, 4 * self.B, "length_out")
                 if abs(e.length_out - e.next_pos) < 4 * self.B:
                     raise ValueError("length_out: overlaps next_pos")
-        if e.budget > self._reserved:
+        try:
+            self._run("bsa_cache_evict", e)
+        except BsaError as x:
+            if x.code != 3:  # too small a workspace, found before anything is launched
+                raise
             self.reserve(e.budget)
-        self._run("bsa_cache_evict", e)
+            self._run("bsa_cache_evict", e)
         return scores_out, pos_out, length_out
 
     def status(self, clear=False):

@@ -657,6 +657,23 @@ def test_a_captured_graph_keeps_its_workspace_when_the_cache_takes_a_larger_one(
     assert cache.status(clear=True) == 11 and cache.status() == 0
 
 
+def test_an_eviction_takes_no_more_workspace_than_it_needs():
+    """A capacity of 2^20 slots a head: one slot's lists fit any workspace, half of them do not."""
+    k = torch.zeros(4, 64, 8, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(2, 1 << 14, dtype=torch.int32, device="cuda")
+    table[:, 1], table[:, 2] = 1, 2
+    cache = bsa.PagedCache(k, k.clone(), table, torch.tensor([129, 100], dtype=torch.int32, device="cuda"))
+    score, pos = torch.rand(2, 8, 1 << 20, device="cuda"), torch.zeros(2, 8, 1 << 20, dtype=torch.int32, device="cuda")
+    nxt = torch.full((2,), 5, dtype=torch.int32, device="cuda")
+    before = cache.workspace.nbytes
+    for budget in ((1 << 20) - 1, 1 << 20, (1 << 31) - 1, 128):
+        cache.evict(score, pos, nxt, budget)
+        assert cache.workspace.nbytes == before
+    assert cache.length.tolist() == [128, 100]
+    cache.evict(score, pos, nxt, 1 << 19)
+    assert cache.workspace.nbytes >= 4 * 4 * 16 << 19 and cache.status() == 0 and cache.length.tolist() == [128, 100]
+
+
 def test_a_workspace_outlives_its_cache_on_another_stream():
     st = Setup([3000, 4000], 4, 8, 2, 128, 128, seed=72)
     want = st.cache().attend(st.q, st.tree)
