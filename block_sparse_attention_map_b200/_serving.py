@@ -366,7 +366,8 @@ class PagedCache:
     """A paged key/value cache and the calls around it.
 
     ``k``, ``v`` [n_pages, page_size, H_kv, D] (bf16 or fp16, the head dimension
-    contiguous), ``page_table`` int32 [B, max_pages], ``length`` int32 [B]: the
+    contiguous), ``page_table`` int32 [B, max_pages] (rows that hold the same pages
+    are fine, a row broadcast over the sequences is not), ``length`` int32 [B]: the
     slots in use.  Slot s of sequence b is row s mod page_size of page
     page_table[b, s // page_size].  The tensors are kept, not copied: change
     ``length`` in place as tokens are accepted.  Only :meth:`append` and
@@ -390,6 +391,9 @@ class PagedCache:
                 (page_table.shape[1] > 1 and page_table.stride(1) != 1):
             raise ValueError("page_table: expected int32 [B, max_pages] on the cache's device, contiguous rows")
         self.B, self.max_pages = page_table.shape
+        if self.B > 1 and page_table.stride(0) < self.max_pages:
+            # (0 would mean contiguous rows to the library, which would read past a broadcast row's end)
+            raise ValueError("page_table: every sequence needs a row of its own memory (one row for all is not taken)")
         self.capacity = self.max_pages * self.page_size
         c = self._c = Cache(self.n_pages, self.page_size, self.H_kv, self.D, DTYPE[self.dtype], self.B, self.max_pages)
         c.k, c.v = k.data_ptr(), v.data_ptr()
