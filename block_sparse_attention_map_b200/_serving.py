@@ -9,6 +9,7 @@ device.  Wrong arguments raise ValueError here or BsaError from the library."""
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import Optional
 
 import torch
@@ -177,6 +178,34 @@ def _check_apart(a, b, same, span_x, span_out, name):
         raise ValueError(f"{name}: overlaps an input without being it")
 
 
+def _apart_rules(xs, xt, ys, yt):
+    """Where a tensor and another one of these shapes and strides share no element
+    although their spans overlap (head ranges of one fused tensor, say): the outer
+    strides of both are multiples of a period, the inner extents of both fit it, and
+    within it they lie apart.  A (period, extent, other's extent) a way to split them."""
+    if 0 in xs or 0 in ys:
+        return ()
+    x, y = ([(st, n) for st, n in zip(t, s) if n > 1] for s, t in ((xs, xt), (ys, yt)))
+    rules = []
+    for cut in sorted({st for st, _ in x + y if st > 1}):
+        period = math.gcd(*(st for st, _ in x + y if st >= cut))
+        ex, ey = (1 + sum((n - 1) * st for st, n in z if st < cut) for z in (x, y))
+        if ex + ey <= period:
+            rules.append((period, ex, ey))
+    return tuple(rules)
+
+
+def _overlap(a, span_a, b, span_b, rules):
+    """Whether tensors at addresses ``a`` and ``b`` may share an element."""
+    if a >= b + 2 * span_b or b >= a + 2 * span_a:
+        return False
+    for period, ea, eb in rules:
+        at = (b - a) // 2 % period
+        if ea <= at <= period - eb:
+            return False
+    return True
+
+
 def _check_flat(a, b, nbytes, name):
     """As :func:`_check_apart` for two contiguous tensors of one size."""
     if a < b + nbytes and b < a + nbytes and a != b:
@@ -191,7 +220,8 @@ def _pair_layout(xs, xt, os, ot, name):
 
 
 def _rotate_layout(qs, qt, qos, qot, ks, kt, kos, kot, ps, pt, fs, axs, dtype, layout, inverse):
-    """A rotation's argument blocks, but for the addresses, and its inputs' and outputs' spans."""
+    """A rotation's argument blocks, but for the addresses, its inputs' and outputs' spans, and
+    when k and q_out, q and k_out, and the outputs are apart."""
     xs = qs if qs is not None else ks
     if len(xs) != 4:
         raise ValueError("q and k are [B, S, H, D] tensors")
@@ -209,7 +239,10 @@ def _rotate_layout(qs, qt, qos, qot, ks, kt, kos, kot, ps, pt, fs, axs, dtype, l
         t.k_stride[:], t.ko_stride[:] = k[0], k[1]
     if len(fs) != 1 or axs != fs:
         raise ValueError("inv_freq and axis: expected one entry a pair")
-    return t, _rope_layout(B, S, ps, pt, fs[0], layout, inverse), q and q[2:], k and k[2:]
+    cross = None
+    if q is not None and k is not None:
+        cross = _apart_rules(ks, kt, qos, qot), _apart_rules(qs, qt, kos, kot), _apart_rules(qos, qot, kos, kot)
+    return t, _rope_layout(B, S, ps, pt, fs[0], layout, inverse), q and q[2:], k and k[2:], cross
 
 
 def _rotate(q, k, pos, inv_freq, axis, layout, inverse, q_out, k_out):
@@ -236,19 +269,19 @@ def _rotate(q, k, pos, inv_freq, axis, layout, inverse, q_out, k_out):
         kp, kop = k.data_ptr(), k_out.data_ptr()
     args = (qs, qt, qos, qot, ks, kt, kos, kot, pos.shape, pos.stride(), inv_freq.shape, axis.shape, DTYPE[kind], layout,
             inverse)
-    t, r, qa, ka = _layout(args, lambda: _rotate_layout(*args))
+    t, r, qa, ka, cross = _layout(args, lambda: _rotate_layout(*args))
     if qa is not None:
         _check_apart(qp, qop, *qa, "q_out")
     if ka is not None:
         _check_apart(kp, kop, *ka, "k_out")
-        if qa is not None:
-            # in place, q and k (and both outputs) may lie side by side in one tensor, each head its own
-            if qop != qp:
-                _check_apart(kp, qop, False, ka[1], qa[2], "q_out")
-            if kop != kp:
-                _check_apart(qp, kop, False, qa[1], ka[2], "k_out")
-            if qop == kop and qa[2] > 0:
-                raise ValueError("q_out and k_out are one tensor")
+    if cross is not None:
+        # (in place, q and k may lie side by side in one tensor, and so may the outputs)
+        if _overlap(kp, ka[1], qop, qa[2], cross[0]):
+            raise ValueError("q_out: overlaps k")
+        if _overlap(qp, qa[1], kop, ka[2], cross[1]):
+            raise ValueError("k_out: overlaps q")
+        if _overlap(qop, qa[2], kop, ka[2], cross[2]):
+            raise ValueError("q_out and k_out overlap")
     _call("bsa_rope", index, _stream_of(index), t, _rope_args(r, pos, inv_freq, axis), qp, qop, kp, kop)
     return q_out, k_out
 
@@ -291,16 +324,18 @@ def tree_words(parents):
 
 
 def _append_layout(ks, kt, vs, vt, qs, qt, qos, qot, ps, pt, fs, axs, layout, B, H_kv, D, dtype):
-    """An append's argument blocks, but for the addresses, and the spans of q and its output."""
+    """An append's argument blocks, but for the addresses, the spans of q and its output, and the
+    spans of k and v with when they are apart from that output."""
     if len(ks) != 4 or ks[0] != B or ks[2] != H_kv or ks[3] != D or vs != ks:
         raise ValueError(f"k and v: expected [{B}, T, {H_kv}, {D}]")
     T = ks[1]
     t = Tokens(B, T, H_kv, H_kv, D, dtype)
     t.k_stride[:], t.v_stride[:] = _strides(ks, kt, "k"), _strides(vs, vt, "v")
     q = r = None
-    spans = _span(ks, kt), _span(vs, vt)
+    cross = None
     if qs is not None:
         q = _pair_layout(qs, qt, qos, qot, "q")
+        cross = tuple((_span(s, st), _apart_rules(s, st, qos, qot)) for s, st in ((ks, kt), (vs, vt)))
         if qs[0] != B or qs[1] != T or qs[3] != D:
             raise ValueError("q must be [B, T, H, D] of the same tokens")
         t.H = qs[2]
@@ -309,7 +344,7 @@ def _append_layout(ks, kt, vs, vt, qs, qt, qos, qot, ps, pt, fs, axs, layout, B,
         if len(fs) != 1 or axs != fs:
             raise ValueError("inv_freq and axis: expected one entry a pair")
         r = _rope_layout(B, T, ps, pt, fs[0], layout, False)
-    return t, r, q and q[2:], spans
+    return t, r, q and q[2:], cross
 
 
 class CacheWorkspace:
@@ -479,16 +514,16 @@ class PagedCache:
             ps, pt, fs, axs = pos.shape, pos.stride(), inv_freq.shape, axis.shape
         args = (k.shape, k.stride(), v.shape, v.stride(), qs, qt, qos, qot, ps, pt, fs, axs, layout, self.B, self.H_kv, self.D,
                 self._c.dtype)
-        proto, rp, qa, spans = _layout(args, lambda: _append_layout(*args))
+        proto, rp, qa, cross = _layout(args, lambda: _append_layout(*args))
         kp, vp = k.data_ptr(), v.data_ptr()
         t = Tokens.from_buffer_copy(proto)
         if n_new is not None:
             t.n_new = _flat(n_new, "n_new", index, torch.int32, (self.B,))
         if qa is not None:
             _check_apart(qp, qop, *qa, "q_out")
-            if qop != qp:
-                _check_apart(kp, qop, False, spans[0], qa[2], "q_out")
-                _check_apart(vp, qop, False, spans[1], qa[2], "q_out")
+            for p, (span, rules), name in ((kp, cross[0], "k"), (vp, cross[1], "v")):
+                if _overlap(p, span, qop, qa[2], rules):
+                    raise ValueError(f"q_out: overlaps {name}")
         if rp is not None:
             r = _rope_args(rp, pos, inv_freq, axis)
         self._run("bsa_cache_append", t, r, qp, qop, kp, vp)
