@@ -172,12 +172,6 @@ def _rope_args(proto, pos, inv_freq, axis):
     return r
 
 
-def _check_apart(a, b, same, span_x, span_out, name):
-    """An output at address ``b`` is its input at ``a`` itself (``same`` strides) or shares no memory with it."""
-    if a < b + 2 * span_out and b < a + 2 * span_x and not (a == b and same):
-        raise ValueError(f"{name}: overlaps an input without being it")
-
-
 def _apart_rules(xs, xt, ys, yt):
     """Where a tensor and another one of these shapes and strides share no element
     although their spans overlap (head ranges of one fused tensor, say): the outer
@@ -206,6 +200,12 @@ def _overlap(a, span_a, b, span_b, rules):
     return True
 
 
+def _check_apart(a, b, same, span_x, span_out, rules, name):
+    """An output at address ``b`` is its input at ``a`` itself (``same`` strides) or shares no element with it."""
+    if not (a == b and same) and _overlap(a, span_x, b, span_out, rules):
+        raise ValueError(f"{name}: overlaps an input without being it")
+
+
 def _check_flat(a, b, nbytes, name):
     """As :func:`_check_apart` for two contiguous tensors of one size."""
     if a < b + nbytes and b < a + nbytes and a != b:
@@ -213,10 +213,12 @@ def _check_flat(a, b, nbytes, name):
 
 
 def _pair_layout(xs, xt, os, ot, name):
-    """A rotation's input and output: (strides, output's strides, whether they are alike, spans)."""
+    """A rotation's input and output: (strides, output's strides, whether they are alike, spans, when they are apart)."""
     if len(xs) != 4 or os != xs:
         raise ValueError(f"{name} and {name}_out: expected [B, S, H, D] tensors of one shape")
-    return _strides(xs, xt, name), _strides(os, ot, name + "_out"), xt == ot, _span(xs, xt), _span(os, ot)
+    same = all(a == b for a, b, n in zip(xt, ot, xs) if n > 1)
+    return (_strides(xs, xt, name), _strides(os, ot, name + "_out"), same, _span(xs, xt), _span(os, ot),
+            _apart_rules(xs, xt, os, ot))
 
 
 def _rotate_layout(qs, qt, qos, qot, ks, kt, kos, kot, ps, pt, fs, axs, dtype, layout, inverse):
@@ -473,17 +475,17 @@ class PagedCache:
         t.qo_stride[:] = _strides(out_shape, out_stride, "out")
         if scale is not None:
             t.scale = scale
-        return t, _span(shape, stride), _span(out_shape, out_stride)
+        return t, _span(shape, stride), _span(out_shape, out_stride), _apart_rules(shape, stride, out_shape, out_stride)
 
     def _queries(self, q, out, tree, n_new, scale):
         """The argument block of q [B, T, H, D] and its options, checked."""
         shape, stride, out_shape, out_stride = q.shape, q.stride(), out.shape, out.stride()
-        proto, span_q, span_out = _layout(
+        proto, span_q, span_out, rules = _layout(
             ("t", shape, stride, out_shape, out_stride, scale, self.B, self.H_kv, self.D, self._c.dtype),
             lambda: self._token_layout(shape, stride, out_shape, out_stride, scale))
         t = Tokens.from_buffer_copy(proto)
         if out is not q:  # the rows of one token are written while others' are still to be read
-            _check_apart(q.data_ptr(), out.data_ptr(), False, span_q, span_out, "out")
+            _check_apart(q.data_ptr(), out.data_ptr(), False, span_q, span_out, rules, "out")
         if q.dtype != self.dtype or q.get_device() != self._index:
             raise ValueError(f"q: expected a {self.dtype} tensor on cuda:{self._index}")
         if n_new is not None:

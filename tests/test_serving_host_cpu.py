@@ -149,3 +149,23 @@ def test_overlap_is_found_for_any_strides():
                 # (the elements of `big` as 16-bit ones)
                 at = [2 * y.storage_offset() for y in (p, q)]
                 assert not sv._overlap(at[0], sv._span(p.shape, p.stride()), at[1], sv._span(q.shape, q.stride()), rules)
+
+
+def test_an_output_beside_its_input_in_one_tensor_is_taken(calls):
+    x, p = fused(8), spec(5, 2)
+    at = lambda a: x[:, :, a:a + 2]  # noqa: E731
+    sv.rope(at(0), at(2), *p, q_out=at(4), k_out=at(6))
+    cache = paged(B=2)
+    cache.append(at(0), at(2), q=at(4), rope=(*p, "halves"), q_out=at(6))
+    lse, tree = OnCuda(torch.zeros(2, 2, 5)), OnCuda(torch.zeros(2, 5, dtype=torch.int64))
+    cache.attend(at(0), tree=tree, out=at(2), lse=lse)
+    # in place through a view whose strides differ where there is one of a dimension
+    one = OnCuda(torch.zeros(1, 5, 1, 64, dtype=torch.bfloat16))
+    again = OnCuda(one.t.as_strided((1, 5, 1, 64), (64, 64, 128, 1)))
+    sv.rope(one, None, *spec(5), q_out=again)
+    assert calls == ["bsa_rope", "bsa_cache_append", "bsa_cache_attend", "bsa_rope"]
+    for call in (lambda: sv.rope(at(0), None, *p, q_out=x[:, :, 1:3]), lambda: cache.attend(at(0), out=x[:, :, 1:3], lse=lse),
+                 lambda: cache.attend(at(0), out=at(0), lse=lse), lambda: sv.rope(x[:, :4, :2], None, *spec(4, 2), q_out=x[:, 1:, :2])):
+        with pytest.raises(ValueError):
+            call()
+    assert len(calls) == 4
