@@ -475,6 +475,8 @@ class PagedCache:
         t.qo_stride[:] = _strides(out_shape, out_stride, "out")
         if scale is not None:
             t.scale = scale
+            if not 0.0 < t.scale < math.inf:  # (the library would take 1/sqrt(D))
+                raise ValueError(f"scale: expected a positive finite number of 32 bits, got {scale}")
         return t, _span(shape, stride), _span(out_shape, out_stride), _apart_rules(shape, stride, out_shape, out_stride)
 
     def _queries(self, q, out, tree, n_new, scale):
@@ -537,7 +539,7 @@ class PagedCache:
         overlap q.  Token t sees
         the slots below ``length`` and the new tokens of its word in ``tree``
         (int64 [B, T], :func:`tree_words`; None: a chain).  Rows at or past
-        ``n_new`` are written as 0 / -inf."""
+        ``n_new`` are written as 0 / -inf.  ``scale`` > 0; None: 1/sqrt(D)."""
         if out is None:
             out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
         elif out is q:

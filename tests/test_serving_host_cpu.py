@@ -169,3 +169,19 @@ def test_an_output_beside_its_input_in_one_tensor_is_taken(calls):
         with pytest.raises(ValueError):
             call()
     assert len(calls) == 4
+
+
+@pytest.mark.parametrize("scale", [0, 0.0, -0.125, float("nan"), float("inf"), 1e-50, 1e39])
+def test_a_scale_that_is_not_positive_and_finite_is_refused(scale, calls):
+    """The library would take 1/sqrt(D) in its place (None says so here)."""
+    cache, q = paged(B=2), fused(2, S=3)
+    lse, scores = OnCuda(torch.zeros(2, 2, 3)), OnCuda(torch.zeros(2, 2, cache.capacity))
+    with pytest.raises(ValueError, match="scale"):
+        cache.attend(q, out=fused(2, S=3), lse=lse, scale=scale)
+    with pytest.raises(ValueError, match="scale"):
+        cache.weigh(q, lse, scores, scale=scale)
+    assert calls == []
+    for good in (None, 0.125, 3, 1e-30):
+        cache.attend(q, out=fused(2, S=3), lse=lse, scale=good)
+        cache.weigh(q, lse, scores, scale=good)
+    assert len(calls) == 8
