@@ -21,8 +21,9 @@
 //               the S columns).
 //   warps 4-7, 8-11   two softmax groups, one row a thread with its 128 scores in
 //               registers (224 a thread, from the other warps' share): the tile's
-//               maximum, lazy rescale of O, P as 16-bit.  Where the piece has two
-//               row tiles, each group has one; where it has one, the groups take
+//               maximum (P and the sums are relative to it, less kLift), lazy
+//               rescale of O, P as 16-bit.  Where the piece has two row tiles,
+//               each group has one; where it has one, the groups take
 //               the key tiles in turn, each with its own running maximum, sums and
 //               O, and add the two up in the epilogue, each for half the columns
 //               (one group alone left the tensor and load pipes waiting for its
@@ -45,7 +46,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 // nothing is joined: four key tiles one after the other take less than a second
 // launch (8 sequences x 1 token over 400 keys: 12.4 us with it, 11.4 without).
 constexpr int kWholeSlots = 512;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units: tolerate p up to 2^8
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: tolerate p up to 2^8 times what it is lifted to
+// log2 of the P that a running maximum's own key gets: in fp16 the largest P is 2^15, of 2^16 that it holds, so
+// that what rounds to zero are weights below 2^-32 of the heaviest (2^-25 where P starts at 1: a few percent of V
+// over 2^21 keys that lie 18 under one heavy key, which their LSE counts)
+template <bool FP16>
+constexpr float kLift = FP16 ? 7.0f : 0.0f;
 
 struct AttendParams {
   CacheView cache;
@@ -57,7 +63,7 @@ struct AttendParams {
   float scale_log2;
   int box_rows, box_log;  // keys of one TMA box: min(page_size, 128)
   float *part_o;          // [2 * CTAs, 128 * NX, D] unnormalised O of the pieces
-  float4 *part_ml;        // [2 * CTAs, 128 * NX] maximum (log2), sum, sum of rounded weights
+  float4 *part_ml;        // [2 * CTAs, 128 * NX] reference (log2: the maximum less kLift), sum, sum of rounded weights
 };
 
 template <int D, int NX>
@@ -368,8 +374,10 @@ k_attend(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtenso
           for (int q = 0; q < 32; ++q)
 #pragma unroll
             for (int c = 0; c < 4; ++c) mx4[c] = fmaxf(mx4[c], __uint_as_float(sv[c][q]));
-          const float mt = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
-          const bool need = mt > m_ref + kRescaleThreshold;
+          // (exponents as the weights below have them, one rounding: large scores' products lose whole powers of two)
+          const float top = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          const float mt = fmaf(top, p.scale_log2, -kLift<FP16>);
+          const bool need = fmaf(top, p.scale_log2, -m_ref) > kLift<FP16> + kRescaleThreshold;
           const bool resc = need && l > 0.f;
           float alpha = 1.f;
           if (need) {
