@@ -15,10 +15,10 @@
 // tokens x 20 heads 30 us, now 17.)
 //
 // The angle is reduced before any rounding to 32 bits: the frequency in turns
-// is a 64-bit fraction of a turn, so its product with the integer position
-// wraps mod 2^64 to the exact fractional turn (within |pos| * 2^-54 turns, the
-// double-precision frequency's own rounding), of which the top 32 bits go to
-// sincospi.
+// is a 64-bit fraction of a turn (from a two-word product with 1 / (2 pi): of one
+// double the position would multiply its rounding, 3e-3 rad at 10^4 rad a position
+// and position 2^31), so its product with the integer position wraps mod 2^64 to the
+// fractional turn within |pos| * 2^-63 turns, of which the top 32 bits go to sincospi.
 #include "serving.cuh"
 
 namespace bsa {
@@ -35,9 +35,12 @@ __device__ __forceinline__ Pair pair_of(const RopeArgs &a, int p) {
   if (p >= a.n_pairs) return Pair{0, -1};
   const int ax = a.axis[p];
   if (static_cast<unsigned>(ax) >= static_cast<unsigned>(a.n_axes)) return Pair{0, -1};
-  double f = a.inv_freq[p] * 0.15915494309189535;  // 1 / (2 pi)
-  f -= floor(f);
-  return Pair{f >= 0.0 && f < 1.0 ? static_cast<uint64_t>(f * 18446744073709551616.0) : 0ull, ax};
+  // 1 / (2 pi) = kHi + kLo, so the frequency in turns = hi + lo; each word less its nearest integer as a multiple of 2^-64
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
+  const double f = a.inv_freq[p], hi = f * kHi, lo = fma(f, kHi, -hi) + f * kLo;
+  if (!isfinite(f)) return Pair{0, ax};
+  auto fraction = [](double x) { return static_cast<uint64_t>(__double2ll_rn((x - rint(x)) * 18446744073709551616.0)); };
+  return Pair{fraction(hi) + fraction(lo), ax};
 }
 
 __device__ __forceinline__ void turn_of(const RopeArgs &a, const Pair &p, int b, int t, float &c, float &s) {

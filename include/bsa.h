@@ -458,8 +458,10 @@ BSA_API bsa_status bsa_fixed_rows(void *ws, size_t ws_bytes, bsa_stream_t stream
  * for the pairs p < n_pairs; elements at or past 2 n_pairs are copied, and so
  * is a pair whose axis entry lies outside [0, n_axes).  inverse = 1 rotates
  * back by the same angles, which is the gradient: dx = R(-angle) dy.  The angle
- * is reduced to a turn in 64-bit fixed point, so it is as exact at position
- * 2^31 - 1 as at position 1.  A frequency that is not finite counts as 0. */
+ * is reduced to a turn in 64-bit fixed point before any rounding to 32 bits
+ * (within |pos| * 2^-63 turns of the exact product, for frequencies up to 2^40),
+ * so it is as exact at position 2^31 - 1 as at position 1.  A frequency that is
+ * not finite counts as 0. */
 typedef struct bsa_rope_spec {
   int32_t n_axes;          /* 1 .. 8                                              */
   int32_t n_pairs;         /* 1 .. D/2; HALVES: a multiple of 8                   */

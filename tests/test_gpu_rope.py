@@ -263,3 +263,28 @@ def test_empty_calls_do_nothing():
         n = bsa.launch_count()
         y, _ = bsa.rope(q, None, torch.empty(1, B, S, dtype=torch.int32, device="cuda"), freq, axis)
         assert y.shape == q.shape and bsa.launch_count() == n
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "halves"])
+def test_far_positions_of_fast_pairs_keep_the_angle(layout):
+    """Frequencies from far below to far above a turn a position, at positions up to
+    the int32 range, against angles reduced in 60 decimal digits (fp64's own product
+    is off by up to 2^-8 rad here): as exact at 2^31 - 1 as at 1."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    turn = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097493")
+    g = gen(11)
+    q = normal(g, (1, 9, 2, 64), "fp16")
+    places = [0, 1, -1, 7, 2 ** 20 + 1, -(2 ** 24) - 3, 2 ** 31 - 1, -(2 ** 31), 1999999973]
+    freqs = [1.0, 1e-9, -1e-9, 0.3, -0.7, 6.2, 6.283185307179586, 7.0, 100.0, -123.456, 9999.99, 1e4, 12345.678, -1e6 / 7, 2.0 ** 40 / 3, 1e15]
+    freq = torch.tensor(freqs, dtype=torch.float64, device="cuda")
+    axis = torch.zeros(16, dtype=torch.int32, device="cuda")
+    y, _ = bsa.rope(q, None, torch.tensor([[places]], dtype=torch.int32, device="cuda"), freq, axis, layout)
+    back, _ = bsa.rope_bwd(y, None, torch.tensor([[places]], dtype=torch.int32, device="cuda"), freq, axis, layout)
+    angle = np.array([[float(Decimal(p) * Decimal(f) % turn) for f in freqs] for p in places])[None, :, None]
+    for x, got, s in ((f64(q), y, 1.0), (f64(y), back, -1.0)):
+        ref = np.array(x)
+        i, j = (slice(0, 32, 2), slice(1, 32, 2)) if layout == "interleaved" else (slice(0, 16), slice(16, 32))
+        a, b = np.array(x[..., i]), np.array(x[..., j])
+        ref[..., i], ref[..., j] = a * np.cos(angle) - s * b * np.sin(angle), s * a * np.sin(angle) + b * np.cos(angle)
+        check_rotated(got, torch.from_numpy(x), ref, "fp16")
