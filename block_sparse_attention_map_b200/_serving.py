@@ -309,7 +309,9 @@ def rope_bwd(dq, dk, pos, inv_freq, axis, layout="interleaved", q_out=None, k_ou
 def tree_words(parents):
     """Tree words (int64 [B, T], bit j of word t: token t sees token j) from each
     token's parent (int [B, T]; -1: it follows the cache; a parent comes before
-    its children).  A token sees its ancestors and itself."""
+    its children).  A token sees its ancestors and itself.  Made on the host: a call
+    waits for ``parents`` and cannot be captured into a graph; a captured step takes
+    the words as an input."""
     B, T = parents.shape
     if T > MAX_TREE:
         raise ValueError(f"at most {MAX_TREE} tokens")

@@ -2,6 +2,8 @@
 work is cut makes the difference, against the fp64 oracle."""
 
 import math
+import os
+import re
 
 import numpy as np
 import pytest
@@ -72,3 +74,87 @@ def test_scores_so_large_that_their_products_lose_powers_of_two(dtype, keys):
                 assert (np.abs(f64(out)[b, t, h] - want) <= HALF_STEP[dtype] * np.abs(want)).all()
                 assert abs(f64(lse)[b, h, t] - s[first]) <= 2.0 ** -16 * abs(s[first])
     assert checked > 40
+
+
+# ------------------------------------------------------------------ the serving step that README shows
+
+def readme_step():
+    """The block of README that makes a PagedCache."""
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    return next(b for b in re.findall(r"```python\n(.*?)```", text, re.S) if "PagedCache" in b)
+
+
+def test_the_readme_step_of_drafted_trees():
+    """Three steps as README has them, on drafted trees whose accepted branch is not
+    their first tokens, against an fp64 model of each head's keys: what is weighed are
+    the accepted rows, over the keys that their softmax went over."""
+    step = compile(readme_step(), "README.md", "exec")
+    B, H, H_kv, D, page, T = 2, 4, 2, 64, 64, 7
+    st = Setup([4093, 300], T, H, H_kv, D, page, "bf16", seed=80, spare=16)
+    parents = torch.tensor([[-1, 0, 0, 2, 2, 4, 1], [-1, -1, 1, 2, 0, 3, 4]])
+    paths, counts = [[0, 2, 4, 5], [1, 2, 3, 5]], [[4, 2], [3, 4], [4, 1]]
+    depth = torch.tensor([[0, 1, 1, 2, 2, 3, 2], [0, 0, 1, 2, 1, 3, 2]], dtype=torch.int32, device="cuda")
+    cap = st.table.shape[1] * page
+    inv_freq = 10000.0 ** (-torch.arange(D // 2, dtype=torch.float64, device="cuda") / (D // 2))
+    ns = dict(bsa=bsa, torch=torch, k_pages=st.k, v_pages=st.v, page_table=st.table, length=st.length,
+              inv_freq=inv_freq, axis=torch.zeros(D // 2, dtype=torch.int32, device="cuda"), parents=parents.cuda(),
+              path=torch.tensor(paths, device="cuda"), scores=torch.rand(B, H_kv, cap, generator=st.g, device="cuda"),
+              key_pos=torch.arange(cap, device="cuda", dtype=torch.int32).expand(B, H_kv, -1).contiguous(),
+              next_pos=st.length.clone())
+    for b in range(B):
+        ns["scores"][b, :, st.lengths[b]:] = 0
+    seq = [[x[:n] for x, n in zip(st.seqs(w), st.lengths)] for w in (st.k, st.v)]
+    keys, values = ([[list(seq[i][b][:, h]) for h in range(H_kv)] for b in range(B)] for i in range(2))
+    score = [[list(f64(ns["scores"])[b, h, :st.lengths[b]]) for h in range(H_kv)] for b in range(B)]
+    place = [[list(range(st.lengths[b])) for _ in range(H_kv)] for b in range(B)]
+    tree = oracle.words_or_chain(bsa.tree_words(parents).tolist(), B, T)
+    evicted = 0
+    for count in counts:
+        q, k, v = (normal(st.g, (B, T, n, D), "bf16") for n in (H, H_kv, H_kv))
+        ns.update(q_new=q, k_new=k, v_new=v, pos=(ns["next_pos"][:, None] + depth)[None].contiguous(),
+                  accepted=torch.tensor(count, dtype=torch.int32, device="cuda"))
+        rq, rk = (f64(x) for x in bsa.rope(q, k, ns["pos"], inv_freq, ns["axis"], "halves"))
+        at, before = ns["pos"][0].tolist(), ns["next_pos"].tolist()
+        exec(step, ns)
+        cache = ns["cache"]
+        assert cache.status() == 0
+        for b in range(B):
+            n, L = count[b], len(keys[b][0])
+            path = paths[b][:n]
+            for h in range(H_kv):
+                mk, mv = np.array(keys[b][h] + list(rk[b, :, h])), np.array(values[b][h] + list(f64(v)[b, :, h]))
+                weight = np.zeros(L + T)
+                for t in range(T):
+                    seen = np.array([j < L or (tree[b][t] >> (j - L)) & 1 == 1 for j in range(L + T)])
+                    for x in (2 * h, 2 * h + 1):
+                        s = np.where(seen, st.scale * (mk @ rq[b, t, x]), -np.inf)
+                        w = np.exp(s - s.max())
+                        w /= w.sum()
+                        O, mass = w @ mv, w @ np.abs(mv)
+                        err = np.abs(f64(ns["o"])[b, t, x] - O)
+                        e = exponent_tolerance(rq[b, t, x], [mk], st.scale)
+                        assert (err <= attend_tolerance(O, mass, L + T, 5.0, "bf16") + 2 * e * mass).all()
+                        if t in path:
+                            weight += w
+                # the accepted rows see the cache and one another's tokens: all of their weight lands on kept tokens
+                assert np.isclose(weight[:L].sum() + weight[[L + t for t in path]].sum(), 2 * n)
+                keys[b][h] += [rk[b, t, h] for t in path]
+                values[b][h] += [f64(v)[b, t, h] for t in path]
+                place[b][h] += [at[b][t] for t in path]
+                score[b][h] = [a + w for a, w in zip(score[b][h] + [0.0] * n, list(weight[:L]) + [weight[L + t] for t in path])]
+                src = oracle.evict_sources(score[b][h], place[b][h], len(keys[b][h]), 4096, 4, 256, before[b] + n)
+                evicted += len(keys[b][h]) - len(src)
+                for m in (keys, values, place, score):
+                    m[b][h] = [m[b][h][i] for i in src]
+        assert ns["length"].tolist() == [len(keys[b][0]) for b in range(B)]
+        assert ns["next_pos"].tolist() == [a + n for a, n in zip(before, count)]
+        for b in range(B):
+            s = np.arange(len(keys[b][0]))
+            rows = st.table_np[b][s // page], s % page
+            for h in range(H_kv):
+                assert ns["key_pos"][b, h, :len(s)].tolist() == place[b][h]
+                assert np.array_equal(f64(st.k)[rows][:, h], np.array(keys[b][h]))
+                assert np.array_equal(f64(st.v)[rows][:, h], np.array(values[b][h]))
+                # each weight off by the factor exp(+-(its exponent's and the lse's error)), fp32 sums of them and the score
+                assert np.allclose(f64(ns["scores"])[b, h, :len(s)], score[b][h], rtol=2.0 ** -18, atol=2.0 ** -18)
+    assert evicted == 2 * (4093 + 11 - 4096)
