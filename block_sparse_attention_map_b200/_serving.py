@@ -251,6 +251,8 @@ def _rotate(q, k, pos, inv_freq, axis, layout, inverse, q_out, k_out):
     x = q if q is not None else k
     if x is None:
         raise ValueError("give q, k or both")
+    if (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("q_out without q, or k_out without k")
     kind, index = x.dtype, x.get_device()
     if index < 0 or kind not in DTYPE:
         raise ValueError("q and k are [B, S, H, D] bf16 or fp16 CUDA tensors")
@@ -509,6 +511,8 @@ class PagedCache:
             if y is not None and (y.dtype != kind or y.get_device() != index):
                 raise ValueError(f"k, v, q and q_out: expected {kind} tensors on cuda:{index}")
         qs = qt = qos = qot = ps = pt = fs = axs = layout = qp = qop = r = None
+        if q is None and q_out is not None:
+            raise ValueError("q_out without q")
         if q is not None:
             if q_out is None:
                 q_out = torch.empty(q.shape, dtype=kind, device=self.device)

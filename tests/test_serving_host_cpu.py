@@ -185,3 +185,13 @@ def test_a_scale_that_is_not_positive_and_finite_is_refused(scale, calls):
         cache.attend(q, out=fused(2, S=3), lse=lse, scale=good)
         cache.weigh(q, lse, scores, scale=good)
     assert len(calls) == 8
+
+
+def test_an_output_without_its_input_is_refused(calls):
+    """It would come back as it was given, unwritten."""
+    x, p, cache = fused(2), spec(5, 2), paged(B=2)
+    for call in (lambda: sv.rope(x, None, *p, q_out=fused(2), k_out=fused(2)), lambda: sv.rope(None, x, *p, q_out=fused(2), k_out=fused(2)),
+                 lambda: sv.rope_bwd(x, None, *p, q_out=fused(2), k_out=fused(2)), lambda: cache.append(x, x, q_out=fused(2))):
+        with pytest.raises(ValueError, match="without"):
+            call()
+    assert calls == []
