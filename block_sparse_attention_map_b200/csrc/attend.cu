@@ -5,8 +5,9 @@
 // The T * G rows of a kv head's group (row = t * G + g) share its keys, so K and
 // V are read once for up to 256 of them: one or two 128-row tiles (NX) against
 // 128-key tiles.  Up to about 200 rows the floor is HBM (4 D bytes a key): 6.4 TB/s
-// at 4 sequences x 1 token over 65536 keys, 5.6 at 16 x 32 tokens x 4 heads a group
-// over 33002 (151 us); 860 TFLOP/s at 256 rows.
+// at 4 sequences x 1 token, 40 heads on 8, over 65536 keys (166 us), 5.5 at 16 x 32
+// tokens, 16 on 4, over up to 33002 (152 us; called among others with inputs that
+// change 178); at 256 rows 880 TFLOP/s (4 x 64 tokens, 32 on 8, 65536 keys, 310 us).
 //
 // k_attend: one CTA per SM.  The (sequence, kv head, row group, key tile) list is
 // cut into equal runs, one a CTA, whatever the lengths are (they are read on the
@@ -27,10 +28,10 @@
 //               the key tiles in turn, each with its own running maximum, sums and
 //               O, and add the two up in the epilogue, each for half the columns
 //               (one group alone left the tensor and load pipes waiting for its
-//               chain of latencies: 187 -> 148 us, 16 sequences x 32 tokens x 4
-//               heads a group over 33002 keys; key tiles taken as two halves, to
-//               overlap more, spent more on the barriers: 182 against 148 us at
-//               24000 keys).
+//               chain of latencies and took 1.26 times as long, 16 sequences x 32
+//               tokens x 4 heads a group over 33002 keys; key tiles taken as two
+//               halves, to overlap more, spent more on the barriers: 1.23 times
+//               at 24000 keys).
 // V of what no row may see (0 * NaN is NaN in the product): infinities and NaN past
 // the new tokens are taken out of the tile in shared memory, and so are those of a
 // new token, which the epilogue of the rows that see the token adds back.
@@ -61,7 +62,7 @@ struct AttendParams {
   int64_t qs[3], os[3];
   float *lse;
   float scale_log2;
-  int box_rows, box_log;  // keys of one TMA box: min(page_size, 128)
+  int box_log;            // log2 of the keys of one TMA box: min(page_size, 128)
   float *part_o;          // [2 * CTAs, 128 * NX, D] unnormalised O of the pieces
   float4 *part_ml;        // [2 * CTAs, 128 * NX] reference (log2: the maximum less kLift), sum, sum of rounded weights
 };
@@ -575,6 +576,8 @@ __global__ void __launch_bounds__(256) k_attend_join(const AttendParams p, int c
   const int h = in ? static_cast<int>(i % p.tok.H) : 0, t = in ? static_cast<int>(i / p.tok.H % p.tok.T) : 0;
   const int b = in ? static_cast<int>(i / p.tok.H / p.tok.T) : 0;
   uint32_t a;
+  // (lengths and counts, before the wait: k_attend lets this kernel start only past its own wait, when what wrote
+  // them is done)
   const Runs runs(total_work<kTile * NX>(p.cache, p.tok, lane, false, b, &a), ctas);
   const Seq<kTile * NX> s = sequence<kTile * NX>(p.cache, p.tok, b, false);
   uint16_t *orow = p.out + b * p.os[0] + t * p.os[1] + h * p.os[2] + lane * E;
@@ -737,7 +740,6 @@ cudaError_t launch_attend(const AttendArgs &a, const CUtensorMap &tk, const CUte
   p.lse = a.lse;
   p.scale_log2 = a.scale * kLog2e;
   p.box_log = std::min(a.cache.page_log, 7);
-  p.box_rows = 1 << p.box_log;
   p.part_ml = reinterpret_cast<float4 *>(a.scratch);
   p.part_o = reinterpret_cast<float *>(a.scratch + static_cast<size_t>(2 * kMaxCtas) * (2 * kTile) * 16);
   const int ctas = std::min(sms, kMaxCtas);

@@ -76,7 +76,9 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 // ---------------------------------------------------------------- launchers
 // Every kernel of these is launched with programmatic serialization and waits for
 // the stream's preceding kernel before it touches global memory, so its set-up
-// runs under that kernel's end.  Only k_attend and k_evict_select let their own
+// runs under that kernel's end.  (k_attend_join alone reads before its wait, and
+// only the lengths and counts: k_attend, which starts it, has waited for whatever
+// wrote them and writes neither.)  Only k_attend and k_evict_select let their own
 // second kernel start early; no other kernel of the stream ever starts before one
 // of these is done.
 //

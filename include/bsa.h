@@ -574,7 +574,8 @@ BSA_API bsa_status bsa_cache_append(const bsa_cache *cache, const bsa_tokens *to
  * [B, H, T] contiguous.
  * A row that sees nothing, and every row t >= n_new[b], is written as 0 / -inf.
  * K and V of what a row does not see never reach it, NaN and infinities
- * included.  The same inputs give the same bits.
+ * included.  The same inputs give the same bits (of all sequences: where a long
+ * sequence is cut goes by every length of the call, and its last bits with it).
  * Errors as for bsa_cache_append; INVALID_ARG also for T > 64, UNSUPPORTED for
  * H / H_kv > 128, for more than 65536 sequences and for 2^29 or more tiles of 128 slots over all sequences, key
  * heads and groups of 128 rows. */
