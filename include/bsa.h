@@ -538,7 +538,8 @@ typedef struct bsa_evict_spec {
   const int32_t *pos_in;
   float *score_out;
   int32_t *pos_out;
-  int32_t *length_out;     /* device [B]; the cache's length or apart from it      */
+  int32_t *length_out;     /* device [B]; the cache's length, or apart from it and
+                              from next_pos                                       */
 } bsa_evict_spec;
 
 /* Rotates q [B, T, H, D] into q_out and k [B, T, H_kv, D] into k_out, either
@@ -560,7 +561,8 @@ BSA_API bsa_status bsa_cache_workspace_size(const bsa_cache *cache, int32_t budg
 
 /* The new tokens into the cache: k (rotated when `rope` is given) and v into the
  * slots length[b] + t, t < n_new[b]; q (NULL to leave it out), every row of it,
- * rotated into q_out (q_out = q: in place).  One launch.  Errors as for
+ * rotated into q_out (q_out = q: in place; q_out shares no element with k or v,
+ * nor with a q that it is not).  One launch.  Errors as for
  * bsa_rope, with INVALID_ARG also for tokens that do not match the cache and
  * WORKSPACE_TOO_SMALL. */
 BSA_API bsa_status bsa_cache_append(const bsa_cache *cache, const bsa_tokens *tok, const bsa_rope_spec *rope,
